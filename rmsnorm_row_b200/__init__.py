@@ -6,7 +6,10 @@ this package is a thin binding over it:
 * the C entry points under their own names (``fused_norm_create``,
   ``fused_norm_validate``, ``fused_norm_launch``, ``fused_norm_destroy``, ...) and
   the ctypes structures ``fn_config`` / ``fn_operand`` / ``fn_args``;
-* tensor-level ops ``fused_residual_norm_scale_shift`` and ``norm_scale_shift``.
+* tensor-level ops ``fused_residual_norm_scale_shift`` and ``norm_scale_shift``;
+* the operators next to them in a transformer block (include/block_ops.h):
+  ``fused_residual_norm_scale_shift_quant`` and ``norm_scale_shift_quant`` (the same rows as
+  e4m3 with a scale per row).
 
 The library is loaded on first use: every entry point raises ImportError if it has not
 been built (``python -m rmsnorm_row_b200.build``); there is no fallback implementation.
@@ -18,6 +21,7 @@ from ._abi import (FN_ERR_CUDA, FN_ERR_INVALID_ARG, FN_ERR_MISALIGNED, FN_ERR_UN
                    fused_norm_launch, fused_norm_plan, fused_norm_status_string,
                    fused_norm_validate, fused_norm_version, load)
 from .api import build_args, fused_residual_norm_scale_shift, norm_scale_shift
+from .norm_quant import fused_residual_norm_scale_shift_quant, norm_scale_shift_quant
 
 __all__ = [
     "FN_OK", "FN_ERR_INVALID_ARG", "FN_ERR_UNSUPPORTED", "FN_ERR_MISALIGNED", "FN_ERR_CUDA",
@@ -25,4 +29,5 @@ __all__ = [
     "fused_norm_destroy", "fused_norm_get_config", "fused_norm_last_cuda_error",
     "fused_norm_launch", "fused_norm_plan", "fused_norm_status_string", "fused_norm_validate",
     "fused_norm_version", "build_args", "fused_residual_norm_scale_shift", "norm_scale_shift",
+    "fused_residual_norm_scale_shift_quant", "norm_scale_shift_quant",
 ]

@@ -1,0 +1,101 @@
+"""ctypes view of include/block_ops.h (argument marshalling only; the library is the one of
+``_abi``, and loading it fails loudly when it has not been built)."""
+from __future__ import annotations
+
+import ctypes
+import threading
+from typing import Dict, Tuple
+
+import torch
+
+from . import _abi
+from ._abi import fn_operand
+
+BO_BF16, BO_FP16, BO_E4M3, BO_FP32 = 0, 1, 2, 3
+DTYPE_CODES = {torch.bfloat16: BO_BF16, torch.float16: BO_FP16, torch.float8_e4m3fn: BO_E4M3,
+               torch.float32: BO_FP32}
+
+_int, _i64, _ptr, _dbl = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_double
+
+
+class nq_config(ctypes.Structure):
+    _fields_ = [("D", _int), ("is_rms", _int), ("has_residual", _int), ("has_gate", _int),
+                ("has_weight", _int), ("has_bias", _int), ("affine_fp32", _int),
+                ("has_modulation", _int), ("eps", _dbl)]
+
+
+class nq_args(ctypes.Structure):
+    _fields_ = [("B", _i64), ("L", _i64), ("tokens_per_frame", _i64),
+                ("x", fn_operand), ("residual", fn_operand), ("gate", fn_operand),
+                ("scale", fn_operand), ("shift", fn_operand),
+                ("weight", _ptr), ("bias", _ptr),
+                ("q", _ptr), ("q_stride_b", _i64), ("q_stride_l", _i64),
+                ("row_scale", _ptr),
+                ("r", _ptr), ("r_stride_b", _i64), ("r_stride_l", _i64)]
+
+
+# operator -> (config, args); each has create / validate / launch / destroy
+OPERATORS = {"norm_quant": (nq_config, nq_args)}
+EXPORTED = tuple(f"{op}_{call}" for op in OPERATORS for call in ("create", "validate", "launch", "destroy")) + (
+    "block_ops_status_string", "block_ops_last_cuda_error")
+
+_declared = None
+
+
+def load() -> ctypes.CDLL:
+    """The loaded library with the prototypes of include/block_ops.h."""
+    global _declared
+    if _declared is None:
+        lib = _abi.load()
+        P = ctypes.POINTER
+        for op, (config, args) in OPERATORS.items():
+            getattr(lib, f"{op}_create").argtypes = [P(_ptr), P(config)]
+            getattr(lib, f"{op}_validate").argtypes = [_ptr, P(args)]
+            getattr(lib, f"{op}_launch").argtypes = [_ptr, P(args), _ptr]
+            getattr(lib, f"{op}_destroy").argtypes = [_ptr]
+            for call in ("create", "validate", "launch", "destroy"):
+                getattr(lib, f"{op}_{call}").restype = _int
+        lib.block_ops_status_string.argtypes = [_int]
+        lib.block_ops_status_string.restype = ctypes.c_char_p
+        lib.block_ops_last_cuda_error.argtypes = []
+        lib.block_ops_last_cuda_error.restype = _int
+        _declared = lib
+    return _declared
+
+
+def check(status: int, what: str) -> None:
+    """Raises FusedNormError for any status but FN_OK."""
+    if status == _abi.FN_OK:
+        return
+    detail = load().block_ops_status_string(status).decode()
+    if status == _abi.FN_ERR_CUDA:
+        detail += f" (cudaError {load().block_ops_last_cuda_error()})"
+    raise _abi.FusedNormError(status, what, detail)
+
+
+_handles: Dict[Tuple, int] = {}
+_handles_lock = threading.Lock()
+
+
+def handle(op: str, key: Tuple, make_config) -> int:
+    """The operator's handle for a configuration, created once per process."""
+    key = (op,) + key
+    h = _handles.get(key)
+    if h is None:
+        with _handles_lock:
+            h = _handles.get(key)
+            if h is None:
+                cfg, out = make_config(), ctypes.c_void_p()
+                check(getattr(load(), f"{op}_create")(ctypes.byref(out), ctypes.byref(cfg)), f"{op}_create")
+                h = _handles[key] = out.value
+    return h
+
+
+def launch(op: str, h: int, args, device: torch.device, stream) -> None:
+    """One launch on `stream` (default: the current stream of `device`), with `device` current
+    for the call."""
+    with torch.cuda.device(device):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        status = getattr(load(), f"{op}_launch")(h, ctypes.byref(args), int(stream.cuda_stream))
+    check(status, f"{op}_launch")

@@ -2,7 +2,7 @@
 
     python -m rmsnorm_row_b200.build          # or: python rmsnorm_row_b200/build.py
 
-Each .cu under csrc/ compiles on its own (in parallel) with
+Each .cu under csrc/ and csrc/block/ compiles on its own (in parallel) with
 ``-gencode arch=compute_100a,code=sm_100a``; the objects link into one shared
 library with the CUDA runtime linked statically, so loading the library needs no
 GPU and no CUDA shared libraries beyond the driver at launch time.
@@ -52,7 +52,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    srcs = glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
+    srcs = glob.glob(os.path.join(CSRC, "**", "*"), recursive=True) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
     return any(os.path.getmtime(s) > t for s in srcs)
 
 
@@ -60,7 +60,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int = 4) -> st
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    srcs = sorted(glob.glob(os.path.join(CSRC, "**", "*.cu"), recursive=True))
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
     tmp = LIB + ".tmp"
