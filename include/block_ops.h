@@ -89,6 +89,85 @@ fn_status norm_quant_validate(norm_quant_t h, const nq_args* a);
 fn_status norm_quant_launch(norm_quant_t h, const nq_args* a, fn_stream_t stream);
 fn_status norm_quant_destroy(norm_quant_t h);
 
+/* ---- rope_norm --------------------------------------------------------------------------
+ *
+ * Rows are tokens: x is (B, L, H, hd), a token has one position per axis.
+ *
+ *   n = x * rho * weight         rho = 1 / sqrt(mean(x^2) + eps) over the head's hd channels
+ *                                (BO_NORM_HEAD; weight of hd values) or over all H * hd of the
+ *                                token (BO_NORM_ALL; weight of H * hd); n = x (BO_NORM_NONE)
+ *   P = section[0] + ... pairs of every head turn, the other hd - 2 P channels pass:
+ *   (y0, y1) = (n0 cos a - n1 sin a, n0 sin a + n1 cos a)
+ *   a = position[axis of the pair] * freq(pair)
+ *
+ * Pair i is channels (2 i, 2 i + 1), or (i, P + i) with half_pairs. The first section[0] pairs
+ * follow axis 0, the next section[1] axis 1, and so on. The i-th of a section's m pairs has
+ * freq = theta^(-i / m); with shared_frequencies pair i of all P has theta^(-i / P).
+ * Angles are reduced in fp64 (an error of at most |position| 2^-52 turns), all else is fp32,
+ * each output is rounded once. A mean square that fp32 does not hold is taken again in fp64.
+ *
+ * The gradient, of the same handle: with dn the grad turned back,
+ *   dx = rho (w dn - x rho^2 mean(w dn x)),  dweight = sum over tokens (and heads, for
+ * BO_NORM_HEAD) of dn x rho, in fp32 per thread and fp64 across threads, in a fixed order.
+ */
+typedef struct rope_norm_s* rope_norm_t;
+
+typedef enum { BO_NORM_NONE = 0, BO_NORM_HEAD = 1, BO_NORM_ALL = 2 } bo_norm;
+
+typedef struct {
+  int dtype;       /* x, grad, y, dx: BO_BF16 or BO_FP16 */
+  int heads, head_dim; /* head_dim: a multiple of 16 up to 512; heads * head_dim <= 16384 */
+  int axes;        /* 1 .. 4 */
+  int section[4];  /* pairs of each axis, >= 1 each; their sum P <= head_dim / 2, and P % 8 == 0
+                      with half_pairs */
+  int norm;        /* bo_norm */
+  int has_weight;  /* needs a norm */
+  int weight_fp32; /* weight is fp32 (otherwise dtype) */
+  int half_pairs, shared_frequencies;
+  int index64;     /* positions are int64_t (otherwise int32_t) */
+  double theta;    /* finite, > 0 */
+  double eps;      /* finite, >= 0 */
+} rn_config;
+
+/* Element (b, l, h, c) lies at ptr[b * stride_b + l * stride_l + h * stride_h + c]; strides are
+ * multiples of 8 elements, pointers 16-byte aligned. */
+typedef struct {
+  const void* ptr;
+  int64_t stride_b, stride_l, stride_h;
+} rn_rows;
+
+typedef struct {
+  int64_t B, L;
+  rn_rows x;
+  const void* positions;     /* (b, l, axis) at [b * stride_b + l * stride_l + axis] */
+  int64_t pos_stride_b, pos_stride_l;
+  const void* weight;
+  rn_rows y;                 /* written; may be x, element for element */
+} rn_args;
+
+typedef struct {
+  int64_t B, L;
+  rn_rows grad, x;           /* x.ptr NULL for BO_NORM_NONE */
+  const void* positions;
+  int64_t pos_stride_b, pos_stride_l;
+  const void* weight;
+  rn_rows dx;                /* written; may be grad or x, element for element */
+  float* dweight;            /* has_weight: written whole, zeros when there are no tokens */
+  void* workspace;           /* 16-byte aligned, rope_norm_backward_workspace bytes, needed until
+                                the launch has run; NULL when that is 0 */
+  uint64_t workspace_bytes;
+} rn_backward_args;
+
+fn_status rope_norm_create(rope_norm_t* out, const rn_config* cfg);
+fn_status rope_norm_validate(rope_norm_t h, const rn_args* a);
+fn_status rope_norm_launch(rope_norm_t h, const rn_args* a, fn_stream_t stream);
+/* Bytes of workspace for a backward launch over B * L tokens, on any device. */
+fn_status rope_norm_backward_workspace(rope_norm_t h, int64_t B, int64_t L, uint64_t* bytes);
+fn_status rope_norm_backward_validate(rope_norm_t h, const rn_backward_args* a);
+/* One kernel launch, and a second one that sums dweight. */
+fn_status rope_norm_backward_launch(rope_norm_t h, const rn_backward_args* a, fn_stream_t stream);
+fn_status rope_norm_destroy(rope_norm_t h);
+
 #ifdef __cplusplus
 }
 #endif

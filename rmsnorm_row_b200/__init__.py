@@ -9,7 +9,8 @@ this package is a thin binding over it:
 * tensor-level ops ``fused_residual_norm_scale_shift`` and ``norm_scale_shift``;
 * the operators next to them in a transformer block (include/block_ops.h):
   ``fused_residual_norm_scale_shift_quant`` and ``norm_scale_shift_quant`` (the same rows as
-  e4m3 with a scale per row).
+  e4m3 with a scale per row), ``rope_norm`` and ``rope_norm_backward`` (q/k norm with rotary
+  positions over several axes).
 
 The library is loaded on first use: every entry point raises ImportError if it has not
 been built (``python -m rmsnorm_row_b200.build``); there is no fallback implementation.
@@ -22,6 +23,7 @@ from ._abi import (FN_ERR_CUDA, FN_ERR_INVALID_ARG, FN_ERR_MISALIGNED, FN_ERR_UN
                    fused_norm_validate, fused_norm_version, load)
 from .api import build_args, fused_residual_norm_scale_shift, norm_scale_shift
 from .norm_quant import fused_residual_norm_scale_shift_quant, norm_scale_shift_quant
+from .rope import rope_norm, rope_norm_backward
 
 __all__ = [
     "FN_OK", "FN_ERR_INVALID_ARG", "FN_ERR_UNSUPPORTED", "FN_ERR_MISALIGNED", "FN_ERR_CUDA",
@@ -30,4 +32,5 @@ __all__ = [
     "fused_norm_launch", "fused_norm_plan", "fused_norm_status_string", "fused_norm_validate",
     "fused_norm_version", "build_args", "fused_residual_norm_scale_shift", "norm_scale_shift",
     "fused_residual_norm_scale_shift_quant", "norm_scale_shift_quant",
+    "rope_norm", "rope_norm_backward",
 ]

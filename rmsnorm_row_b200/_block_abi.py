@@ -34,10 +34,39 @@ class nq_args(ctypes.Structure):
                 ("r", _ptr), ("r_stride_b", _i64), ("r_stride_l", _i64)]
 
 
-# operator -> (config, args); each has create / validate / launch / destroy
-OPERATORS = {"norm_quant": (nq_config, nq_args)}
-EXPORTED = tuple(f"{op}_{call}" for op in OPERATORS for call in ("create", "validate", "launch", "destroy")) + (
-    "block_ops_status_string", "block_ops_last_cuda_error")
+c_int4 = _int * 4
+
+
+class rn_config(ctypes.Structure):
+    _fields_ = [("dtype", _int), ("heads", _int), ("head_dim", _int), ("axes", _int), ("section", c_int4),
+                ("norm", _int), ("has_weight", _int), ("weight_fp32", _int), ("half_pairs", _int),
+                ("shared_frequencies", _int), ("index64", _int), ("theta", _dbl), ("eps", _dbl)]
+
+
+class rn_rows(ctypes.Structure):
+    _fields_ = [("ptr", _ptr), ("stride_b", _i64), ("stride_l", _i64), ("stride_h", _i64)]
+
+
+class rn_args(ctypes.Structure):
+    _fields_ = [("B", _i64), ("L", _i64), ("x", rn_rows), ("positions", _ptr), ("pos_stride_b", _i64),
+                ("pos_stride_l", _i64), ("weight", _ptr), ("y", rn_rows)]
+
+
+class rn_backward_args(ctypes.Structure):
+    _fields_ = [("B", _i64), ("L", _i64), ("grad", rn_rows), ("x", rn_rows), ("positions", _ptr),
+                ("pos_stride_b", _i64), ("pos_stride_l", _i64), ("weight", _ptr), ("dx", rn_rows),
+                ("dweight", _ptr), ("workspace", _ptr), ("workspace_bytes", ctypes.c_uint64)]
+
+
+# operator -> (config, {launch and its validate: args})
+OPERATORS = {
+    "norm_quant": (nq_config, {"launch": nq_args}),
+    "rope_norm": (rn_config, {"launch": rn_args, "backward_launch": rn_backward_args}),
+}
+EXPORTED = tuple(f"{op}_{call}" for op, (_, calls) in OPERATORS.items()
+                 for name in calls for call in (name, name.replace("launch", "validate"))) + tuple(
+    f"{op}_{call}" for op in OPERATORS for call in ("create", "destroy")) + (
+    "rope_norm_backward_workspace", "block_ops_status_string", "block_ops_last_cuda_error")
 
 _declared = None
 
@@ -48,13 +77,15 @@ def load() -> ctypes.CDLL:
     if _declared is None:
         lib = _abi.load()
         P = ctypes.POINTER
-        for op, (config, args) in OPERATORS.items():
+        for op, (config, calls) in OPERATORS.items():
             getattr(lib, f"{op}_create").argtypes = [P(_ptr), P(config)]
-            getattr(lib, f"{op}_validate").argtypes = [_ptr, P(args)]
-            getattr(lib, f"{op}_launch").argtypes = [_ptr, P(args), _ptr]
             getattr(lib, f"{op}_destroy").argtypes = [_ptr]
-            for call in ("create", "validate", "launch", "destroy"):
-                getattr(lib, f"{op}_{call}").restype = _int
+            for name, args in calls.items():
+                getattr(lib, f"{op}_{name}").argtypes = [_ptr, P(args), _ptr]
+                getattr(lib, f"{op}_{name.replace('launch', 'validate')}").argtypes = [_ptr, P(args)]
+        lib.rope_norm_backward_workspace.argtypes = [_ptr, _i64, _i64, P(ctypes.c_uint64)]
+        for name in EXPORTED:
+            getattr(lib, name).restype = _int
         lib.block_ops_status_string.argtypes = [_int]
         lib.block_ops_status_string.restype = ctypes.c_char_p
         lib.block_ops_last_cuda_error.argtypes = []
@@ -91,11 +122,18 @@ def handle(op: str, key: Tuple, make_config) -> int:
     return h
 
 
-def launch(op: str, h: int, args, device: torch.device, stream) -> None:
-    """One launch on `stream` (default: the current stream of `device`), with `device` current
-    for the call."""
+def rope_norm_workspace(h: int, B: int, L: int) -> int:
+    """Bytes of workspace of a backward launch."""
+    n = ctypes.c_uint64()
+    check(load().rope_norm_backward_workspace(h, B, L, ctypes.byref(n)), "rope_norm_backward_workspace")
+    return n.value
+
+
+def launch(op: str, h: int, args, device: torch.device, stream, call: str = "launch") -> None:
+    """One call on `stream` (default: the current stream of `device`), with `device` current
+    for it."""
     with torch.cuda.device(device):
         if stream is None:
             stream = torch.cuda.current_stream(device)
-        status = getattr(load(), f"{op}_launch")(h, ctypes.byref(args), int(stream.cuda_stream))
-    check(status, f"{op}_launch")
+        status = getattr(load(), f"{op}_{call}")(h, ctypes.byref(args), int(stream.cuda_stream))
+    check(status, f"{op}_{call}")

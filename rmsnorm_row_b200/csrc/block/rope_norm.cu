@@ -1,0 +1,353 @@
+// Host side of rope_norm (checks, shapes, launches) and the sum of dweight's partials.
+#include <atomic>
+#include <cmath>
+#include <cstring>
+#include <new>
+#include <utility>
+
+#include "host_checks.h"
+#include "rope_norm_kernel.cuh"
+
+namespace block_ops {
+namespace {
+
+// dweight[c] = the partials' sum over CTAs, in fp64, in their order: eight slices of the CTAs
+// per column, then the slices.
+__global__ void __launch_bounds__(256) sum_partials(const float* partial, int parts, int n, float* out) {
+  __shared__ double slices[8][32];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  double s = 0.0;
+  if (c < n)
+#pragma unroll 4
+    for (int i = threadIdx.y; i < parts; i += 8) s += (double)__ldcg(partial + (size_t)i * n + c);
+  slices[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < n) {
+    for (int i = 1; i < 8; ++i) s += slices[i][threadIdx.x];
+    out[c] = (float)s;
+  }
+}
+
+struct RopeShape {
+  int W, T, G, nh, rows_per_cta;
+};
+
+// Lanes of a head, threads of a row and heads of a thread. Rows of more than 32 lanes take the
+// number of heads per thread (1, 2 or 4) that leaves the fewest idle lanes, 2 where it is even.
+RopeShape rope_shape(int H, int hd) {
+  RopeShape s;
+  s.W = 1;
+  while (s.W < hd / 16) s.W *= 2;
+  if (H * s.W <= 32) {
+    s.nh = 1, s.T = 1;
+    while (s.T < H * s.W) s.T *= 2;
+  } else {
+    s.T = 0;
+    for (int nh : {2, 1, 4}) {
+      const int T = ((H + nh - 1) / nh * s.W + 31) / 32 * 32;
+      if (T <= kRopeThreads && (s.T == 0 || T * nh < s.T * s.nh)) s.T = T, s.nh = nh;
+    }
+  }
+  s.G = s.T / s.W;
+  s.rows_per_cta = s.T > 32 ? 1 : kSharedRows / s.T;
+  return s;
+}
+
+}  // namespace
+}  // namespace block_ops
+
+using namespace block_ops;
+
+struct rope_norm_s {
+  rn_config cfg;
+  RopeShape shape;
+  RopeKernel forward, backward;
+  RopeParams base;  // the parts of the launch parameters that the configuration settles
+  size_t smem[2];  // of the two kernels
+  mutable std::atomic<int> resident[2] = {{0}, {0}};  // CTAs per SM of the two kernels, once known
+};
+
+namespace {
+
+int weight_values(const rn_config& c) { return c.norm == BO_NORM_ALL ? c.heads * c.head_dim : c.head_dim; }
+bool sums_dweight(const rn_config& c) { return c.has_weight != 0; }
+
+bool rows_extent(const rn_rows& r, int64_t B, int64_t L, const rn_config& c, Span* out) {
+  const int64_t n[3] = {B, L, c.heads}, s[3] = {r.stride_b, r.stride_l, r.stride_h};
+  const int64_t e = extent_of(n, s, c.head_dim);
+  if (e < 0) return false;
+  *out = bytes_at(r.ptr, (uint64_t)e * 2);
+  return true;
+}
+
+void check_rows(const rn_rows& r, Findings& f) {
+  f.require(r.stride_b >= 0 && r.stride_l >= 0 && r.stride_h >= 0, FN_ERR_INVALID_ARG);
+  f.require(aligned16(r.ptr) && r.stride_b % 8 == 0 && r.stride_l % 8 == 0 && r.stride_h % 8 == 0, FN_ERR_MISALIGNED);
+}
+
+// Output rows: no two (b, l, h) share a byte, whichever of the three strides is the largest.
+void check_out(const rn_rows& r, int64_t B, int64_t L, const rn_config& c, Findings& f) {
+  check_rows(r, f);
+  int64_t n[3] = {B, L, c.heads}, s[3] = {r.stride_b, r.stride_l, r.stride_h};
+  __int128 width = c.head_dim;  // of what the dimensions so far span
+  for (int done = 0; done < 3; ++done) {
+    int at = done;
+    for (int i = done + 1; i < 3; ++i)
+      if (n[at] == 1 || (n[i] > 1 && s[i] < s[at])) at = i;
+    std::swap(n[at], n[done]);
+    std::swap(s[at], s[done]);
+    if (n[done] == 1) continue;
+    f.require((__int128)s[done] >= width, FN_ERR_INVALID_ARG);
+    width += (__int128)(n[done] - 1) * s[done];
+  }
+}
+
+bool same_places(const rn_rows& a, const rn_rows& b, int64_t B, int64_t L, int H) {
+  return a.ptr == b.ptr && (B == 1 || a.stride_b == b.stride_b) && (L == 1 || a.stride_l == b.stride_l) &&
+         (H == 1 || a.stride_h == b.stride_h);
+}
+
+// What both directions check: sizes, positions, weight, the inputs against the output.
+fn_status check(const rope_norm_s* h, int64_t B, int64_t L, const rn_rows* const (&ins)[2], const rn_rows& out,
+                const void* positions, int64_t psb, int64_t psl, const void* weight, const Span& dweight, const Span& work) {
+  const rn_config& c = h->cfg;
+  Findings f;
+  f.require(positions && out.ptr, FN_ERR_INVALID_ARG);
+  f.require((weight != nullptr) == (c.has_weight != 0), FN_ERR_INVALID_ARG);
+  f.require(psb >= 0 && psl >= 0, FN_ERR_INVALID_ARG);
+  f.require(reinterpret_cast<uintptr_t>(positions) % (c.index64 ? 8 : 4) == 0, FN_ERR_MISALIGNED);
+  f.require(aligned16(weight), FN_ERR_MISALIGNED);
+  for (const rn_rows* r : ins)
+    if (r) check_rows(*r, f);
+  check_out(out, B, L, c, f);
+  if (f.status != FN_OK) return f.status;
+
+  Span o;
+  if (!rows_extent(out, B, L, c, &o)) return FN_ERR_INVALID_ARG;
+  const int64_t n[2] = {B, L}, ps[2] = {psb, psl};
+  const int64_t pe = extent_of(n, ps, c.axes);
+  if (pe < 0) return FN_ERR_INVALID_ARG;
+  const Span pos = bytes_at(positions, (uint64_t)pe * (c.index64 ? 8 : 4));
+  const Span w = bytes_at(weight, weight ? (uint64_t)weight_values(c) * (c.weight_fp32 ? 4 : 2) : 0);
+  const Span written[3] = {o, dweight, work};
+  for (int i = 0; i < 3; ++i) {
+    if (overlaps(written[i], pos) || overlaps(written[i], w)) return FN_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(written[i], written[j])) return FN_ERR_INVALID_ARG;
+  }
+  for (const rn_rows* r : ins) {
+    if (!r) continue;
+    Span s;
+    if (!rows_extent(*r, B, L, c, &s)) return FN_ERR_INVALID_ARG;
+    if (overlaps(o, s) && !same_places(*r, out, B, L, c.heads)) return FN_ERR_INVALID_ARG;
+    if (overlaps(dweight, s) || overlaps(work, s)) return FN_ERR_INVALID_ARG;
+  }
+  return FN_OK;
+}
+
+// Sizes alone: FN_OK with *empty set when there is nothing to do.
+fn_status check_sizes(const rope_norm_s* h, int64_t B, int64_t L, bool* empty) {
+  if (B < 0 || L < 0) return FN_ERR_INVALID_ARG;
+  *empty = B == 0 || L == 0;
+  if (*empty) return FN_OK;
+  if (B > kMaxRows || L > kMaxRows || B * L > kMaxRows) return FN_ERR_INVALID_ARG;
+  if ((__int128)B * L * h->cfg.heads * h->cfg.head_dim > kMaxExtent) return FN_ERR_INVALID_ARG;
+  return FN_OK;
+}
+
+fn_status validate(const rope_norm_s* h, const rn_args* a, bool* empty) {
+  if (!h || !a) return FN_ERR_INVALID_ARG;
+  const fn_status s = check_sizes(h, a->B, a->L, empty);
+  if (s != FN_OK || *empty) return s;
+  if (!a->x.ptr) return FN_ERR_INVALID_ARG;
+  const rn_rows* ins[2] = {&a->x, nullptr};
+  return check(h, a->B, a->L, ins, a->y, a->positions, a->pos_stride_b, a->pos_stride_l, a->weight, Span{}, Span{});
+}
+
+int64_t ctas(const rope_norm_s* h, int64_t rows) { return (rows + h->shape.rows_per_cta - 1) / h->shape.rows_per_cta; }
+
+uint64_t workspace_bytes(const rope_norm_s* h, int64_t rows) {
+  if (!sums_dweight(h->cfg) || rows == 0) return 0;
+  const int64_t n = ctas(h, rows);
+  return (uint64_t)(n < kMaxPartials ? n : kMaxPartials) * weight_values(h->cfg) * sizeof(float);
+}
+
+fn_status validate(const rope_norm_s* h, const rn_backward_args* a, bool* empty) {
+  if (!h || !a) return FN_ERR_INVALID_ARG;
+  const rn_config& c = h->cfg;
+  const fn_status s = check_sizes(h, a->B, a->L, empty);
+  if (s != FN_OK) return s;
+  if ((a->dweight != nullptr) != sums_dweight(c)) return FN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(a->dweight) % 4) return FN_ERR_MISALIGNED;
+  if (*empty) return FN_OK;
+  if (!a->grad.ptr || (a->x.ptr != nullptr) != (c.norm != BO_NORM_NONE)) return FN_ERR_INVALID_ARG;
+  const uint64_t need = workspace_bytes(h, a->B * a->L);
+  if (need && (!a->workspace || a->workspace_bytes < need)) return FN_ERR_INVALID_ARG;
+  if (need && !aligned16(a->workspace)) return FN_ERR_MISALIGNED;
+  const rn_rows* ins[2] = {&a->grad, c.norm != BO_NORM_NONE ? &a->x : nullptr};
+  return check(h, a->B, a->L, ins, a->dx, a->positions, a->pos_stride_b, a->pos_stride_l, a->weight,
+               bytes_at(a->dweight, a->dweight ? 4 * (uint64_t)weight_values(c) : 0), bytes_at(a->workspace, need));
+}
+
+RopeRows rows_of(const rn_rows& r) {
+  return RopeRows{static_cast<const uint16_t*>(r.ptr), r.stride_b, r.stride_l, r.stride_h};
+}
+
+// Above 48 KB a kernel's shared memory is asked for, once per device context.
+cudaError_t allow_shared(const rope_norm_s* h, bool back) {
+  if (h->smem[back] <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(back ? h->backward : h->forward, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)h->smem[back]);
+}
+
+// The number of CTAs: what the current device holds at once, at most one per rows_per_cta rows.
+fn_status grid_of(const rope_norm_s* h, bool back, int64_t rows, int* grid) {
+  int per_sm = h->resident[back].load(std::memory_order_relaxed);
+  if (per_sm == 0) {
+    cudaError_t e = allow_shared(h, back);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        &per_sm, back ? h->backward : h->forward, h->shape.T * h->shape.rows_per_cta, h->smem[back]);
+    if (e != cudaSuccess) return launch_status(e);
+    if (per_sm < 1) per_sm = 1;
+    h->resident[back].store(per_sm, std::memory_order_relaxed);
+  }
+  int device = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+  if (e != cudaSuccess) return launch_status(e);
+  int64_t g = (int64_t)per_sm * sms;
+  if (back && sums_dweight(h->cfg) && g > kMaxPartials) g = kMaxPartials;
+  const int64_t n = ctas(h, rows);
+  *grid = (int)(g < n ? g : n);
+  return FN_OK;
+}
+
+fn_status run(const rope_norm_s* h, bool back, int grid, RopeParams& p, int64_t B, int64_t L, const void* positions, int64_t psb,
+              int64_t psl, const void* weight, const rn_rows& out, cudaStream_t stream) {
+  p.out = rows_of(out);
+  p.positions = positions, p.pos_sb = psb, p.pos_sl = psl;
+  p.weight = weight;
+  p.rows = (uint32_t)(B * L), p.L = (uint32_t)L;
+  p.div_L = fused_norm_impl::make_div_u32(p.L);
+  const cudaError_t e = allow_shared(h, back);
+  if (e != cudaSuccess) return launch_status(e);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(h->shape.T * h->shape.rows_per_cta);
+  cfg.dynamicSmemBytes = h->smem[back];
+  cfg.stream = stream;
+  return launch_status(cudaLaunchKernelEx(&cfg, back ? h->backward : h->forward, p));
+}
+
+}  // namespace
+
+extern "C" {
+
+fn_status rope_norm_create(rope_norm_t* out, const rn_config* cfg) {
+  if (!out || !cfg) return FN_ERR_INVALID_ARG;
+  const rn_config& c = *cfg;
+  for (int v : {c.has_weight, c.weight_fp32, c.half_pairs, c.shared_frequencies, c.index64})
+    if (!is_flag(v)) return FN_ERR_INVALID_ARG;
+  if (c.norm < BO_NORM_NONE || c.norm > BO_NORM_ALL) return FN_ERR_INVALID_ARG;
+  if (c.has_weight && c.norm == BO_NORM_NONE) return FN_ERR_INVALID_ARG;
+  if (c.weight_fp32 && !c.has_weight) return FN_ERR_INVALID_ARG;
+  if (!std::isfinite(c.theta) || c.theta <= 0.0 || !std::isfinite(c.eps) || c.eps < 0.0 || c.eps > 0x1p100) return FN_ERR_INVALID_ARG;
+  if (c.axes < 1 || c.axes > 4 || c.heads < 1 || c.head_dim < 1) return FN_ERR_INVALID_ARG;
+  int64_t pairs = 0;
+  for (int a = 0; a < c.axes; ++a) {
+    if (c.section[a] < 1) return FN_ERR_INVALID_ARG;
+    pairs += c.section[a];
+  }
+  if (pairs > c.head_dim / 2) return FN_ERR_INVALID_ARG;
+  if (c.dtype != BO_BF16 && c.dtype != BO_FP16) return FN_ERR_UNSUPPORTED;
+  if (c.head_dim % 16 || c.head_dim > 2 * kMaxPairs || (int64_t)c.heads * c.head_dim > 16384) return FN_ERR_UNSUPPORTED;
+  if (c.half_pairs && pairs % 8) return FN_ERR_UNSUPPORTED;
+  rope_norm_s* h = new (std::nothrow) rope_norm_s;
+  if (!h) return FN_ERR_INVALID_ARG;
+  h->cfg = c;
+  const RopeShape s = h->shape = rope_shape(c.heads, c.head_dim);
+  auto pick = [&](bool back) {
+    return c.dtype == BO_FP16 ? pick_rope<true>(s.nh, c.norm, c.half_pairs, back, back && sums_dweight(c))
+                              : pick_rope<false>(s.nh, c.norm, c.half_pairs, back, back && sums_dweight(c));
+  };
+  h->forward = pick(false), h->backward = pick(true);
+  for (int back = 0; back < 2; ++back)
+    h->smem[back] = rope_shared_bytes(s.rows_per_cta, (int)pairs, s.T * s.rows_per_cta, s.nh, back != 0);
+  RopeParams& p = h->base;
+  std::memset(&p, 0, sizeof(p));
+  p.H = c.heads, p.hd = c.head_dim, p.units = c.head_dim / 16, p.pairs = (int)pairs;
+  p.W = s.W, p.T = s.T, p.G = s.G;
+  p.index64 = c.index64, p.weight_fp32 = c.weight_fp32;
+  p.weight_sh = c.norm == BO_NORM_ALL ? c.head_dim : 0;
+  p.inv_n64 = 1.0 / (c.norm == BO_NORM_ALL ? c.heads * c.head_dim : c.head_dim), p.eps64 = c.eps;
+  p.inv_n = (float)p.inv_n64, p.eps = (float)c.eps;
+  int i = 0;
+  for (int a = 0; a < c.axes; ++a)
+    for (int k = 0; k < c.section[a]; ++k, ++i) {
+      const double part = c.shared_frequencies ? (double)i / (double)pairs : (double)k / c.section[a];
+      p.turns[i] = std::pow(c.theta, -part) / 6.283185307179586476925;
+      p.axis[i] = (uint8_t)a;
+    }
+  *out = h;
+  return FN_OK;
+}
+
+fn_status rope_norm_validate(rope_norm_t h, const rn_args* a) {
+  bool empty;
+  return validate(h, a, &empty);
+}
+
+fn_status rope_norm_launch(rope_norm_t h, const rn_args* a, fn_stream_t stream) {
+  bool empty;
+  fn_status s = validate(h, a, &empty);
+  if (s != FN_OK || empty) return s;
+  int grid;
+  s = grid_of(h, false, a->B * a->L, &grid);
+  if (s != FN_OK) return s;
+  RopeParams p = h->base;
+  p.x = rows_of(a->x);
+  return run(h, false, grid, p, a->B, a->L, a->positions, a->pos_stride_b, a->pos_stride_l, a->weight, a->y,
+             reinterpret_cast<cudaStream_t>(stream));
+}
+
+fn_status rope_norm_backward_workspace(rope_norm_t h, int64_t B, int64_t L, uint64_t* bytes) {
+  if (!h || !bytes) return FN_ERR_INVALID_ARG;
+  bool empty;
+  const fn_status s = check_sizes(h, B, L, &empty);
+  if (s == FN_OK) *bytes = empty ? 0 : workspace_bytes(h, B * L);
+  return s;
+}
+
+fn_status rope_norm_backward_validate(rope_norm_t h, const rn_backward_args* a) {
+  bool empty;
+  return validate(h, a, &empty);
+}
+
+fn_status rope_norm_backward_launch(rope_norm_t h, const rn_backward_args* a, fn_stream_t stream_) {
+  bool empty;
+  fn_status s = validate(h, a, &empty);
+  if (s != FN_OK) return s;
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const int n = weight_values(h->cfg);
+  if (empty)
+    return a->dweight ? launch_status(cudaMemsetAsync(a->dweight, 0, (size_t)n * 4, stream)) : FN_OK;
+  int grid;
+  s = grid_of(h, true, a->B * a->L, &grid);
+  if (s != FN_OK) return s;
+  RopeParams p = h->base;
+  p.x = rows_of(a->x), p.dy = rows_of(a->grad);
+  p.partial = static_cast<float*>(a->workspace);
+  s = run(h, true, grid, p, a->B, a->L, a->positions, a->pos_stride_b, a->pos_stride_l, a->weight, a->dx, stream);
+  if (s != FN_OK || !a->dweight) return s;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((n + 31) / 32);
+  cfg.blockDim = dim3(32, 8);
+  cfg.stream = stream;
+  return launch_status(cudaLaunchKernelEx(&cfg, sum_partials, (const float*)p.partial, grid, n, a->dweight));
+}
+
+fn_status rope_norm_destroy(rope_norm_t h) {
+  delete h;
+  return FN_OK;
+}
+
+}  // extern "C"
