@@ -168,6 +168,50 @@ fn_status rope_norm_backward_validate(rope_norm_t h, const rn_backward_args* a);
 fn_status rope_norm_backward_launch(rope_norm_t h, const rn_backward_args* a, fn_stream_t stream);
 fn_status rope_norm_destroy(rope_norm_t h);
 
+/* ---- linear_gate ------------------------------------------------------------------------
+ *
+ *   out = residual + gate * act(x W^T + bias)      x (B, L, K), W (N, K), out (B, L, N)
+ *
+ * x and W are both bf16, both fp16 or both e4m3 (then x W^T is x_scale[row] * weight_scale[n]
+ * times the product of the codes, and bias, gate, residual and out are bf16; otherwise they
+ * have x's type). The sum over K and everything after it is fp32; out is rounded once.
+ * act is SiLU z / (1 + e^-z), GELU z Phi(z), its tanh form, or nothing.
+ */
+typedef struct linear_gate_s* linear_gate_t;
+
+typedef enum { BO_ACT_NONE = 0, BO_ACT_SILU = 1, BO_ACT_GELU = 2, BO_ACT_GELU_TANH = 3 } bo_act;
+
+typedef struct {
+  int dtype;          /* BO_BF16, BO_FP16 or BO_E4M3 */
+  int64_t K, N;       /* 8 .. 2^20; N and K multiples of 8, K of 16 for e4m3 */
+  int act;            /* bo_act */
+  int has_bias, has_gate, has_residual;
+} lg_config;
+
+typedef struct {
+  int64_t B, L;
+  int64_t tokens_per_frame;   /* of the gate; as in fn_args */
+  fn_operand x;               /* stride_f 0; strides multiples of 16 bytes */
+  const void* weight;         /* row n at weight + n * weight_stride elements, 16-byte aligned rows */
+  int64_t weight_stride;
+  const void* bias;           /* (N) */
+  fn_operand gate, residual;
+  const float* x_scale;       /* (B, L) contiguous; e4m3 */
+  const float* weight_scale;  /* (N), 16-byte aligned; e4m3 */
+  void* out;                  /* strides in elements, multiples of 8; may be residual, element for element */
+  int64_t out_stride_b, out_stride_l;
+} lg_args;
+
+fn_status linear_gate_create(linear_gate_t* out, const lg_config* cfg);
+fn_status linear_gate_validate(linear_gate_t h, const lg_args* a);
+/* One kernel launch. */
+fn_status linear_gate_launch(linear_gate_t h, const lg_args* a, fn_stream_t stream);
+/* The matrix kernel bounds its internal waits (ten seconds); a launch in which one ran out, a
+ * sign of a broken device, leaves its output incomplete and is counted on its device. Reads the
+ * current device's count (synchronises with its default stream). */
+fn_status linear_gate_timeouts(int* count);
+fn_status linear_gate_destroy(linear_gate_t h);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,7 +10,8 @@ this package is a thin binding over it:
 * the operators next to them in a transformer block (include/block_ops.h):
   ``fused_residual_norm_scale_shift_quant`` and ``norm_scale_shift_quant`` (the same rows as
   e4m3 with a scale per row), ``rope_norm`` and ``rope_norm_backward`` (q/k norm with rotary
-  positions over several axes).
+  positions over several axes) and ``linear_gate_residual`` (matrix product with bias,
+  activation, gate and residual in its epilogue, from 16-bit or e4m3 rows).
 
 The library is loaded on first use: every entry point raises ImportError if it has not
 been built (``python -m rmsnorm_row_b200.build``); there is no fallback implementation.
@@ -22,6 +23,7 @@ from ._abi import (FN_ERR_CUDA, FN_ERR_INVALID_ARG, FN_ERR_MISALIGNED, FN_ERR_UN
                    fused_norm_launch, fused_norm_plan, fused_norm_status_string,
                    fused_norm_validate, fused_norm_version, load)
 from .api import build_args, fused_residual_norm_scale_shift, norm_scale_shift
+from .linear import linear_gate_residual
 from .norm_quant import fused_residual_norm_scale_shift_quant, norm_scale_shift_quant
 from .rope import rope_norm, rope_norm_backward
 
@@ -32,5 +34,5 @@ __all__ = [
     "fused_norm_launch", "fused_norm_plan", "fused_norm_status_string", "fused_norm_validate",
     "fused_norm_version", "build_args", "fused_residual_norm_scale_shift", "norm_scale_shift",
     "fused_residual_norm_scale_shift_quant", "norm_scale_shift_quant",
-    "rope_norm", "rope_norm_backward",
+    "rope_norm", "rope_norm_backward", "linear_gate_residual",
 ]

@@ -58,15 +58,28 @@ class rn_backward_args(ctypes.Structure):
                 ("dweight", _ptr), ("workspace", _ptr), ("workspace_bytes", ctypes.c_uint64)]
 
 
+class lg_config(ctypes.Structure):
+    _fields_ = [("dtype", _int), ("K", _i64), ("N", _i64), ("act", _int), ("has_bias", _int), ("has_gate", _int),
+                ("has_residual", _int)]
+
+
+class lg_args(ctypes.Structure):
+    _fields_ = [("B", _i64), ("L", _i64), ("tokens_per_frame", _i64), ("x", fn_operand), ("weight", _ptr),
+                ("weight_stride", _i64), ("bias", _ptr), ("gate", fn_operand), ("residual", fn_operand),
+                ("x_scale", _ptr), ("weight_scale", _ptr), ("out", _ptr), ("out_stride_b", _i64),
+                ("out_stride_l", _i64)]
+
+
 # operator -> (config, {launch and its validate: args})
 OPERATORS = {
     "norm_quant": (nq_config, {"launch": nq_args}),
     "rope_norm": (rn_config, {"launch": rn_args, "backward_launch": rn_backward_args}),
+    "linear_gate": (lg_config, {"launch": lg_args}),
 }
 EXPORTED = tuple(f"{op}_{call}" for op, (_, calls) in OPERATORS.items()
                  for name in calls for call in (name, name.replace("launch", "validate"))) + tuple(
     f"{op}_{call}" for op in OPERATORS for call in ("create", "destroy")) + (
-    "rope_norm_backward_workspace", "block_ops_status_string", "block_ops_last_cuda_error")
+    "rope_norm_backward_workspace", "linear_gate_timeouts", "block_ops_status_string", "block_ops_last_cuda_error")
 
 _declared = None
 
@@ -84,6 +97,7 @@ def load() -> ctypes.CDLL:
                 getattr(lib, f"{op}_{name}").argtypes = [_ptr, P(args), _ptr]
                 getattr(lib, f"{op}_{name.replace('launch', 'validate')}").argtypes = [_ptr, P(args)]
         lib.rope_norm_backward_workspace.argtypes = [_ptr, _i64, _i64, P(ctypes.c_uint64)]
+        lib.linear_gate_timeouts.argtypes = [P(_int)]
         for name in EXPORTED:
             getattr(lib, name).restype = _int
         lib.block_ops_status_string.argtypes = [_int]

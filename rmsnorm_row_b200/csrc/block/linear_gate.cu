@@ -1,0 +1,257 @@
+// Host side of linear_gate: checks, the choice of a kernel, tensor maps, launches.
+#include <cudaTypedefs.h>
+
+#include <cstring>
+#include <new>
+
+#include "host_checks.h"
+#include "linear_gate_kernel.cuh"
+
+using namespace block_ops;
+
+struct linear_gate_s {
+  lg_config cfg;
+};
+
+namespace {
+
+constexpr int64_t kMaxWidth = 1 << 20;
+
+int element_size(const lg_config& c) { return c.dtype == BO_E4M3 ? 1 : 2; }
+
+fn_status validate(const linear_gate_s* h, const lg_args* a) {
+  if (!h || !a) return FN_ERR_INVALID_ARG;
+  const lg_config& c = h->cfg;
+  const int64_t B = a->B, L = a->L, tpf = a->tokens_per_frame, K = c.K, N = c.N;
+  const bool fp8 = c.dtype == BO_E4M3;
+  const int size = element_size(c), unit = 16 / size;
+  if (B < 0 || L < 0 || tpf < 0) return FN_ERR_INVALID_ARG;
+  if (B == 0 || L == 0) return FN_OK;
+  if (B > kMaxRows || L > kMaxRows || B * L > kMaxRows - 256) return FN_ERR_INVALID_ARG;  // tiles of 256 rows stay in 31 bits
+  if ((__int128)B * L * (K > N ? K : N) > kMaxExtent) return FN_ERR_INVALID_ARG;
+  if (tpf > 0 && L % tpf != 0) return FN_ERR_INVALID_ARG;
+  const int64_t F = tpf > 0 ? L / tpf : 1;
+
+  Findings f;
+  f.require(a->x.ptr && a->weight && a->out, FN_ERR_INVALID_ARG);
+  f.require((a->bias != nullptr) == (c.has_bias != 0) && (a->gate.ptr != nullptr) == (c.has_gate != 0) &&
+                (a->residual.ptr != nullptr) == (c.has_residual != 0),
+            FN_ERR_INVALID_ARG);
+  f.require((a->x_scale != nullptr) == fp8 && (a->weight_scale != nullptr) == fp8, FN_ERR_INVALID_ARG);
+  f.require(a->x.stride_b >= 0 && a->x.stride_l >= 0 && a->x.stride_f == 0, FN_ERR_INVALID_ARG);
+  f.require(aligned16(a->x.ptr) && a->x.stride_b % unit == 0 && a->x.stride_l % unit == 0, FN_ERR_MISALIGNED);
+  f.require(a->weight_stride >= (N > 1 ? K : 0), FN_ERR_INVALID_ARG);
+  f.require(aligned16(a->weight) && a->weight_stride % unit == 0, FN_ERR_MISALIGNED);
+  f.require(aligned16(a->bias) && aligned16(a->weight_scale), FN_ERR_MISALIGNED);
+  f.require(reinterpret_cast<uintptr_t>(a->x_scale) % 4 == 0, FN_ERR_MISALIGNED);
+  if (a->gate.ptr) check_operand(a->gate, tpf > 0, f);
+  if (a->residual.ptr) check_operand(a->residual, tpf > 0, f);
+  check_output(a->out, a->out_stride_b, a->out_stride_l, B, L, N, 8, f);
+  if (f.status != FN_OK) return f.status;
+  // what a tensor map holds: no row that several tokens share, strides below 2^40 bytes
+  if (B * L > kTokens && ((L > 1 && a->x.stride_l == 0) || (B > 1 && a->x.stride_b == 0))) return FN_ERR_UNSUPPORTED;
+  if (a->x.stride_b * size >= (int64_t)1 << 39 || a->x.stride_l * size >= (int64_t)1 << 39 ||
+      a->weight_stride * size >= (int64_t)1 << 39)
+    return FN_ERR_INVALID_ARG;
+
+  const int64_t n[2] = {B, L}, os[2] = {a->out_stride_b, a->out_stride_l}, xs[2] = {a->x.stride_b, a->x.stride_l};
+  const int64_t wn[1] = {N}, ws[1] = {a->weight_stride};
+  const int64_t oe = extent_of(n, os, N), xe = extent_of(n, xs, K), we = extent_of(wn, ws, K);
+  if (oe < 0 || xe < 0 || we < 0) return FN_ERR_INVALID_ARG;
+  const Span out = bytes_at(a->out, (uint64_t)oe * 2);
+  if (overlaps(out, bytes_at(a->x.ptr, (uint64_t)xe * size)) || overlaps(out, bytes_at(a->weight, (uint64_t)we * size)))
+    return FN_ERR_INVALID_ARG;
+  if (a->bias && overlaps(out, bytes_at(a->bias, (uint64_t)N * 2))) return FN_ERR_INVALID_ARG;
+  if (fp8 && (overlaps(out, bytes_at(a->x_scale, (uint64_t)B * L * 4)) || overlaps(out, bytes_at(a->weight_scale, (uint64_t)N * 4))))
+    return FN_ERR_INVALID_ARG;
+  const bool in_place = same_rows(a->residual, a->out, a->out_stride_b, a->out_stride_l, B, L);
+  for (const fn_operand* o : {&a->gate, &a->residual}) {
+    if (!o->ptr) continue;
+    Span s;
+    if (!operand_span(*o, B, F, L, N, 2, &s)) return FN_ERR_INVALID_ARG;
+    if (overlaps(out, s) && !(o == &a->residual && in_place)) return FN_ERR_INVALID_ARG;
+  }
+  return FN_OK;
+}
+
+LinearOperand operand_of(const fn_operand& o) {
+  return LinearOperand{static_cast<const uint16_t*>(o.ptr), o.stride_b, o.stride_f, o.stride_l};
+}
+
+LinearParams make_params(const linear_gate_s* h, const lg_args* a) {
+  LinearParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = a->x.ptr, p.weight = a->weight;
+  p.x_sb = a->x.stride_b, p.x_sl = a->x.stride_l, p.weight_stride = a->weight_stride;
+  p.rows = (uint32_t)(a->B * a->L), p.L = (uint32_t)a->L, p.tpf = (uint32_t)a->tokens_per_frame;
+  p.div_L = fused_norm_impl::make_div_u32(p.L);
+  p.div_tpf = fused_norm_impl::make_div_u32(p.tpf ? p.tpf : 1u);
+  p.N = (uint32_t)h->cfg.N, p.K = (uint32_t)h->cfg.K;
+  p.act = h->cfg.act;
+  p.bias = static_cast<const uint16_t*>(a->bias);
+  p.gate = operand_of(a->gate), p.residual = operand_of(a->residual);
+  p.x_scale = a->x_scale, p.weight_scale = a->weight_scale;
+  p.out = static_cast<uint16_t*>(a->out);
+  p.out_sb = a->out_stride_b, p.out_sl = a->out_stride_l;
+  return p;
+}
+
+// ---- a few tokens ---------------------------------------------------------------------------
+
+template <bool FP8, bool FP16>
+void* token_kernel(int M) {
+  switch (M) {
+    case 1: return (void*)linear_gate_tokens<1, FP8, FP16>;
+    case 2: return (void*)linear_gate_tokens<2, FP8, FP16>;
+    case 3: return (void*)linear_gate_tokens<3, FP8, FP16>;
+    default: return (void*)linear_gate_tokens<4, FP8, FP16>;
+  }
+}
+
+fn_status launch_tokens(const linear_gate_s* h, LinearParams& p, cudaStream_t stream) {
+  const int per_cta = kTokenThreads / 32 * kTokenColumns;
+  void* kernel = h->cfg.dtype == BO_E4M3   ? token_kernel<true, false>(p.rows)
+                 : h->cfg.dtype == BO_FP16 ? token_kernel<false, true>(p.rows)
+                                           : token_kernel<false, false>(p.rows);
+  void* args[] = {&p};
+  return launch_status(cudaLaunchKernel(kernel, dim3((p.N + per_cta - 1) / per_cta), dim3(kTokenThreads), args, 0, stream));
+}
+
+// ---- many rows --------------------------------------------------------------------------------
+
+struct Variant {
+  int cg, bn, shared;
+  void* kernel[3];  // by dtype: bf16, fp16, e4m3
+};
+template <int CG, int BN>
+Variant variant() {
+  return Variant{CG, BN, MatrixShape<CG, BN>::kShared,
+                 {(void*)linear_gate_tiles<CG, BN, false, false>, (void*)linear_gate_tiles<CG, BN, false, true>,
+                  (void*)linear_gate_tiles<CG, BN, true, false>}};
+}
+const Variant kVariants[] = {variant<2, 256>(), variant<1, 256>(), variant<1, 128>(), variant<1, 64>()};
+
+// A row-major matrix of `rows` rows of K elements per batch as boxes of 128 bytes x box_rows.
+fn_status encode(CUtensorMap* m, const lg_config& c, const void* ptr, int64_t rows, int64_t row_stride, int64_t batches,
+                 int64_t batch_stride, int box_rows) {
+  static const auto fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  if (!fn) return launch_status(cudaErrorNotSupported);
+  const int size = element_size(c);
+  const cuuint64_t dims[3] = {(cuuint64_t)c.K, (cuuint64_t)rows, (cuuint64_t)batches};
+  // a single row or batch is never stepped over: any valid stride serves
+  const cuuint64_t strides[2] = {(cuuint64_t)(rows > 1 ? row_stride * size : 16), (cuuint64_t)(batches > 1 ? batch_stride * size : 16)};
+  const cuuint32_t box[3] = {(cuuint32_t)(kStepBytes / size), (cuuint32_t)box_rows, 1}, unit[3] = {1, 1, 1};
+  const CUtensorMapDataType type = c.dtype == BO_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : c.dtype == BO_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUresult r = fn(m, type, 3, const_cast<void*>(ptr), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FN_OK : launch_status(cudaErrorInvalidValue);
+}
+
+fn_status launch_tiles(const linear_gate_s* h, const lg_args* a, LinearParams& p, cudaStream_t stream) {
+  const lg_config& c = h->cfg;
+  int device = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+  if (e != cudaSuccess) return launch_status(e);
+
+  // Rows one after another in memory are one batch; otherwise a tile stays inside a batch.
+  const bool flat = a->B == 1 || a->L == 1 || a->x.stride_b == a->L * a->x.stride_l;
+  const int64_t batches = flat ? 1 : a->B, rows = flat ? a->B * a->L : a->L;
+  const int64_t row_stride = a->L == 1 ? a->x.stride_b : a->x.stride_l;
+
+  const Variant* best = nullptr;
+  int64_t best_cost = 0;
+  for (const Variant& v : kVariants) {
+    const int64_t tm = (rows + kTileM * v.cg - 1) / (kTileM * v.cg) * batches, tn = (c.N + v.bn - 1) / v.bn;
+    const int64_t waves = (tm * tn + sms / v.cg - 1) / (sms / v.cg);
+    // a tile's time: its products, and what does not shrink with it
+    const int64_t cost = waves * (v.bn + (v.cg == 2 ? 0 : 32));
+    if (!best || cost < best_cost) best = &v, best_cost = cost;
+  }
+  const Variant& v = *best;
+  const int size = element_size(c);
+  p.batch_rows = (uint32_t)rows, p.batches = (uint32_t)batches;
+  p.tiles_m = (uint32_t)((rows + kTileM * v.cg - 1) / (kTileM * v.cg)), p.tiles_n = (uint32_t)((c.N + v.bn - 1) / v.bn);
+  const int64_t tiles = (int64_t)p.tiles_m * p.batches * p.tiles_n;
+  if (tiles > kMaxRows) return FN_ERR_INVALID_ARG;
+  p.tiles = (uint32_t)tiles;
+  p.group = 8;
+  p.div_band = fused_norm_impl::make_div_u32(p.group * p.tiles_n);
+  p.div_tiles_m = fused_norm_impl::make_div_u32(p.tiles_m);
+  p.steps = (uint32_t)((c.K * size + kStepBytes - 1) / kStepBytes);
+  // fp32 sums (bit 4), operand types (fp16 0, bf16 1; e4m3 0), N / 8 at bit 17, M / 16 at bit 24
+  const uint32_t type = c.dtype == BO_BF16 ? 1u : 0u;
+  p.idesc = 1u << 4 | type << 7 | type << 10 | (uint32_t)(v.bn / 8) << 17 | (uint32_t)(kTileM * v.cg / 16) << 24;
+
+  CUtensorMap mx, mw;
+  fn_status s = encode(&mx, c, a->x.ptr, rows, row_stride, batches, a->x.stride_b, kTileM);
+  if (s == FN_OK) s = encode(&mw, c, a->weight, c.N, a->weight_stride, 1, 0, v.bn / v.cg);
+  if (s != FN_OK) return s;
+
+  void* kernel = v.kernel[c.dtype];
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.shared);
+  if (e != cudaSuccess) return launch_status(e);
+  const int64_t resident = sms / v.cg;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((tiles < resident ? tiles : resident) * v.cg));
+  cfg.blockDim = dim3(kMatrixThreads);
+  cfg.dynamicSmemBytes = v.shared;
+  cfg.stream = stream;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = v.cg, cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = v.cg > 1 ? 1 : 0;
+  void* args[] = {&p, &mx, &mw};
+  return launch_status(cudaLaunchKernelExC(&cfg, kernel, args));
+}
+
+}  // namespace
+
+extern "C" {
+
+fn_status linear_gate_create(linear_gate_t* out, const lg_config* cfg) {
+  if (!out || !cfg) return FN_ERR_INVALID_ARG;
+  const lg_config& c = *cfg;
+  for (int v : {c.has_bias, c.has_gate, c.has_residual})
+    if (!is_flag(v)) return FN_ERR_INVALID_ARG;
+  if (c.act < BO_ACT_NONE || c.act > BO_ACT_GELU_TANH) return FN_ERR_INVALID_ARG;
+  if (c.dtype != BO_BF16 && c.dtype != BO_FP16 && c.dtype != BO_E4M3) return FN_ERR_UNSUPPORTED;
+  if (c.K < 8 || c.N < 8 || c.K > kMaxWidth || c.N > kMaxWidth || c.N % 8 || c.K % (16 / element_size(c))) return FN_ERR_UNSUPPORTED;
+  linear_gate_s* h = new (std::nothrow) linear_gate_s;
+  if (!h) return FN_ERR_INVALID_ARG;
+  h->cfg = c;
+  *out = h;
+  return FN_OK;
+}
+
+fn_status linear_gate_validate(linear_gate_t h, const lg_args* a) { return validate(h, a); }
+
+fn_status linear_gate_launch(linear_gate_t h, const lg_args* a, fn_stream_t stream) {
+  const fn_status s = validate(h, a);
+  if (s != FN_OK || a->B == 0 || a->L == 0) return s;
+  LinearParams p = make_params(h, a);
+  if (p.rows <= (uint32_t)kTokens) return launch_tokens(h, p, reinterpret_cast<cudaStream_t>(stream));
+  return launch_tiles(h, a, p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+fn_status linear_gate_timeouts(int* count) {
+  if (!count) return FN_ERR_INVALID_ARG;
+  return launch_status(cudaMemcpyFromSymbol(count, linear_gate_gave_up, sizeof(int)));
+}
+
+fn_status linear_gate_destroy(linear_gate_t h) {
+  delete h;
+  return FN_OK;
+}
+
+}  // extern "C"
