@@ -195,7 +195,7 @@ typedef struct {
   const void* weight;         /* row n at weight + n * weight_stride elements, 16-byte aligned rows */
   int64_t weight_stride;
   const void* bias;           /* (N) */
-  fn_operand gate, residual;
+  fn_operand gate, residual;  /* residual: one row per token, stride_f 0 */
   const float* x_scale;       /* (B, L) contiguous; e4m3 */
   const float* weight_scale;  /* (N), 16-byte aligned; e4m3 */
   void* out;                  /* strides in elements, multiples of 8; may be residual, element for element */

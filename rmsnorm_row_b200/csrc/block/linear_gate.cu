@@ -2,6 +2,7 @@
 #include <cudaTypedefs.h>
 
 #include <cstring>
+#include <cstdlib>
 #include <new>
 
 #include "host_checks.h"
@@ -45,13 +46,17 @@ fn_status validate(const linear_gate_s* h, const lg_args* a) {
   f.require(aligned16(a->bias) && aligned16(a->weight_scale), FN_ERR_MISALIGNED);
   f.require(reinterpret_cast<uintptr_t>(a->x_scale) % 4 == 0, FN_ERR_MISALIGNED);
   if (a->gate.ptr) check_operand(a->gate, tpf > 0, f);
-  if (a->residual.ptr) check_operand(a->residual, tpf > 0, f);
+  if (a->residual.ptr) {
+    check_operand(a->residual, false, f);
+    f.require((L == 1 || a->residual.stride_l > 0) && (B == 1 || a->residual.stride_b > 0), FN_ERR_INVALID_ARG);
+  }
   check_output(a->out, a->out_stride_b, a->out_stride_l, B, L, N, 8, f);
   if (f.status != FN_OK) return f.status;
   // what a tensor map holds: no row that several tokens share, strides below 2^40 bytes
   if (B * L > kTokens && ((L > 1 && a->x.stride_l == 0) || (B > 1 && a->x.stride_b == 0))) return FN_ERR_UNSUPPORTED;
   if (a->x.stride_b * size >= (int64_t)1 << 39 || a->x.stride_l * size >= (int64_t)1 << 39 ||
-      a->weight_stride * size >= (int64_t)1 << 39)
+      a->weight_stride * size >= (int64_t)1 << 39 || a->out_stride_b >= (int64_t)1 << 38 || a->out_stride_l >= (int64_t)1 << 38 ||
+      a->residual.stride_b >= (int64_t)1 << 38 || a->residual.stride_l >= (int64_t)1 << 38)
     return FN_ERR_INVALID_ARG;
 
   const int64_t n[2] = {B, L}, os[2] = {a->out_stride_b, a->out_stride_l}, xs[2] = {a->x.stride_b, a->x.stride_l};
@@ -90,6 +95,7 @@ LinearParams make_params(const linear_gate_s* h, const lg_args* a) {
   p.act = h->cfg.act;
   p.bias = static_cast<const uint16_t*>(a->bias);
   p.gate = operand_of(a->gate), p.residual = operand_of(a->residual);
+  p.has_residual = h->cfg.has_residual;
   p.x_scale = a->x_scale, p.weight_scale = a->weight_scale;
   p.out = static_cast<uint16_t*>(a->out);
   p.out_sb = a->out_stride_b, p.out_sl = a->out_stride_l;
@@ -131,9 +137,12 @@ Variant variant() {
 }
 const Variant kVariants[] = {variant<2, 256>(), variant<1, 256>(), variant<1, 128>(), variant<1, 64>()};
 
-// A row-major matrix of `rows` rows of K elements per batch as boxes of 128 bytes x box_rows.
-fn_status encode(CUtensorMap* m, const lg_config& c, const void* ptr, int64_t rows, int64_t row_stride, int64_t batches,
-                 int64_t batch_stride, int box_rows) {
+// A matrix of `rows` rows of `width` elements per batch, as a tensor map of boxes.
+struct Matrix {
+  const void* ptr;
+  int64_t width, rows, row_stride, batches, batch_stride;
+};
+fn_status encode(CUtensorMap* m, int dtype, const Matrix& a, int box_width, int box_rows, CUtensorMapSwizzle swizzle) {
   static const auto fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -143,16 +152,17 @@ fn_status encode(CUtensorMap* m, const lg_config& c, const void* ptr, int64_t ro
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
   }();
   if (!fn) return launch_status(cudaErrorNotSupported);
-  const int size = element_size(c);
-  const cuuint64_t dims[3] = {(cuuint64_t)c.K, (cuuint64_t)rows, (cuuint64_t)batches};
+  const int size = dtype == BO_E4M3 ? 1 : 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)a.width, (cuuint64_t)a.rows, (cuuint64_t)a.batches};
   // a single row or batch is never stepped over: any valid stride serves
-  const cuuint64_t strides[2] = {(cuuint64_t)(rows > 1 ? row_stride * size : 16), (cuuint64_t)(batches > 1 ? batch_stride * size : 16)};
-  const cuuint32_t box[3] = {(cuuint32_t)(kStepBytes / size), (cuuint32_t)box_rows, 1}, unit[3] = {1, 1, 1};
-  const CUtensorMapDataType type = c.dtype == BO_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                   : c.dtype == BO_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const CUresult r = fn(m, type, 3, const_cast<void*>(ptr), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint64_t strides[2] = {(cuuint64_t)(a.rows > 1 ? a.row_stride * size : 16),
+                                 (cuuint64_t)(a.batches > 1 ? a.batch_stride * size : 16)};
+  const cuuint32_t box[3] = {(cuuint32_t)box_width, (cuuint32_t)box_rows, 1}, unit[3] = {1, 1, 1};
+  const CUtensorMapDataType type = dtype == BO_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : dtype == BO_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUresult r = fn(m, type, 3, const_cast<void*>(a.ptr), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FN_OK : launch_status(cudaErrorInvalidValue);
 }
 
@@ -163,10 +173,15 @@ fn_status launch_tiles(const linear_gate_s* h, const lg_args* a, LinearParams& p
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) return launch_status(e);
 
-  // Rows one after another in memory are one batch; otherwise a tile stays inside a batch.
-  const bool flat = a->B == 1 || a->L == 1 || a->x.stride_b == a->L * a->x.stride_l;
+  // Rows at one distance from each other are one batch; otherwise a tile stays inside a batch.
+  auto even = [&](int64_t sb, int64_t sl) { return sb == a->L * sl; };
+  const bool flat = a->B == 1 || a->L == 1 ||
+                    (even(a->x.stride_b, a->x.stride_l) && even(a->out_stride_b, a->out_stride_l) &&
+                     (!c.has_residual || even(a->residual.stride_b, a->residual.stride_l)));
   const int64_t batches = flat ? 1 : a->B, rows = flat ? a->B * a->L : a->L;
-  const int64_t row_stride = a->L == 1 ? a->x.stride_b : a->x.stride_l;
+  auto matrix = [&](const void* ptr, int64_t width, int64_t sb, int64_t sl) {
+    return Matrix{ptr, width, rows, a->L == 1 ? sb : sl, batches, sb};
+  };
 
   const Variant* best = nullptr;
   int64_t best_cost = 0;
@@ -177,6 +192,7 @@ fn_status launch_tiles(const linear_gate_s* h, const lg_args* a, LinearParams& p
     const int64_t cost = waves * (v.bn + (v.cg == 2 ? 0 : 32));
     if (!best || cost < best_cost) best = &v, best_cost = cost;
   }
+  if (getenv("LG_VARIANT")) best = &kVariants[atoi(getenv("LG_VARIANT"))];
   const Variant& v = *best;
   const int size = element_size(c);
   p.batch_rows = (uint32_t)rows, p.batches = (uint32_t)batches;
@@ -184,7 +200,7 @@ fn_status launch_tiles(const linear_gate_s* h, const lg_args* a, LinearParams& p
   const int64_t tiles = (int64_t)p.tiles_m * p.batches * p.tiles_n;
   if (tiles > kMaxRows) return FN_ERR_INVALID_ARG;
   p.tiles = (uint32_t)tiles;
-  p.group = 8;
+  p.group = getenv("LG_GROUP") ? atoi(getenv("LG_GROUP")) : 8;
   p.div_band = fused_norm_impl::make_div_u32(p.group * p.tiles_n);
   p.div_tiles_m = fused_norm_impl::make_div_u32(p.tiles_m);
   p.steps = (uint32_t)((c.K * size + kStepBytes - 1) / kStepBytes);
@@ -192,9 +208,17 @@ fn_status launch_tiles(const linear_gate_s* h, const lg_args* a, LinearParams& p
   const uint32_t type = c.dtype == BO_BF16 ? 1u : 0u;
   p.idesc = 1u << 4 | type << 7 | type << 10 | (uint32_t)(v.bn / 8) << 17 | (uint32_t)(kTileM * v.cg / 16) << 24;
 
-  CUtensorMap mx, mw;
-  fn_status s = encode(&mx, c, a->x.ptr, rows, row_stride, batches, a->x.stride_b, kTileM);
-  if (s == FN_OK) s = encode(&mw, c, a->weight, c.N, a->weight_stride, 1, 0, v.bn / v.cg);
+  const int out_type = c.dtype == BO_FP16 ? BO_FP16 : BO_BF16, per_step = kStepBytes / size;
+  CUtensorMap mx, mw, mo, mr;
+  fn_status s = encode(&mx, c.dtype, matrix(a->x.ptr, c.K, a->x.stride_b, a->x.stride_l), per_step, kTileM, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (s == FN_OK)
+    s = encode(&mw, c.dtype, Matrix{a->weight, c.K, c.N, a->weight_stride, 1, 0}, per_step, v.bn / v.cg, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (s == FN_OK)
+    s = encode(&mo, out_type, matrix(a->out, c.N, a->out_stride_b, a->out_stride_l), kBox, kBox, CU_TENSOR_MAP_SWIZZLE_64B);
+  mr = mo;
+  if (s == FN_OK && c.has_residual)
+    s = encode(&mr, out_type, matrix(a->residual.ptr, c.N, a->residual.stride_b, a->residual.stride_l), kBox, kBox,
+               CU_TENSOR_MAP_SWIZZLE_64B);
   if (s != FN_OK) return s;
 
   void* kernel = v.kernel[c.dtype];
@@ -211,7 +235,7 @@ fn_status launch_tiles(const linear_gate_s* h, const lg_args* a, LinearParams& p
   cluster.val.clusterDim.x = v.cg, cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
   cfg.attrs = &cluster;
   cfg.numAttrs = v.cg > 1 ? 1 : 0;
-  void* args[] = {&p, &mx, &mw};
+  void* args[] = {&p, &mx, &mw, &mo, &mr};
   return launch_status(cudaLaunchKernelExC(&cfg, kernel, args));
 }
 

@@ -4,11 +4,13 @@
 // out = residual + gate * act(x W^T + bias). Many rows are bound by the tensor cores
 // (2 M N K operations against (M + N) K + 2 M N elements), a few tokens by reading W once.
 //
-// Many rows: persistent CTAs or CTA pairs (CG = 2) of six warps. One thread loads 128-byte
+// Many rows: persistent CTAs or CTA pairs (CG = 2) of ten warps. One thread loads 128-byte
 // wide tiles of x and W by TMA into a ring of shared-memory stages, one thread issues the
-// tcgen05 products of a 128 CG x BN tile into TMEM, four warps read the sums back, a row per
+// tcgen05 products of a 128 CG x BN tile into TMEM, eight warps read the sums back, a row per
 // thread, and finish them. TMEM holds two tiles, so the epilogue of one runs under the
-// products of the next. A pair shares W's tile: each CTA loads half of it.
+// products of the next. A pair shares W's tile: each CTA loads half of it. Residual and output
+// pass through shared memory in boxes of 32 x 32: TMA brings a warp's next residual box while
+// the present one is worked on in place, and stores it.
 //
 // A few tokens: every warp streams rows of W past the tokens with 16-byte loads.
 #pragma once
@@ -40,6 +42,7 @@ struct LinearParams {
   int act;
   const uint16_t* bias;
   LinearOperand gate, residual;
+  int has_residual;
   const float *x_scale, *weight_scale;
   uint16_t* out;
   int64_t out_sb, out_sl;
@@ -52,82 +55,133 @@ __device__ __forceinline__ float logistic_times(float z, float e) { return __fdi
 
 template <int N>
 __device__ __forceinline__ void activate(int act, float (&v)[N]) {
+  if (act == BO_ACT_NONE) return;
   if (act == BO_ACT_SILU) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = logistic_times(v[i], v[i]);
   } else if (act == BO_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678118654752f));
-  } else if (act == BO_ACT_GELU_TANH) {  // 1/2 (1 + tanh t) = 1 / (1 + e^-2t)
+  } else {  // 1/2 (1 + tanh t) = 1 / (1 + e^-2t)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float t = 1.5957691216057308f * fmaf(0.044715f * v[i] * v[i], v[i], v[i]);
+      const float t = v[i] * fmaf(v[i] * v[i], 1.5957691216057308f * 0.044715f, 1.5957691216057308f);
       v[i] = logistic_times(v[i], t);
     }
   }
 }
 
-// Where a row's operands lie.
+// A row's token, gate and scale.
 struct RowOut {
-  uint16_t* out;
-  const uint16_t *gate, *residual;
+  uint32_t b, l;
+  const uint16_t* gate;
   float x_scale;
 };
 __device__ __forceinline__ RowOut row_out(const LinearParams& p, uint32_t row) {
   RowOut r;
   const uint32_t b = div_u32(row, p.div_L), l = row - b * p.L;
   const uint32_t f = p.tpf ? div_u32(l, p.div_tpf) : 0u;
-  r.out = p.out + (b * p.out_sb + l * p.out_sl);
+  r.b = b, r.l = l;
   r.gate = p.gate.ptr ? p.gate.ptr + (b * p.gate.sb + f * p.gate.sf + l * p.gate.sl) : nullptr;
-  r.residual = p.residual.ptr ? p.residual.ptr + (b * p.residual.sb + f * p.residual.sf + l * p.residual.sl) : nullptr;
   r.x_scale = p.x_scale ? __ldg(p.x_scale + row) : 1.0f;
   return r;
 }
 
-// Eight columns from n on (n % 8 == 0, n < N): sums to outputs.
-template <bool FP16>
-__device__ __forceinline__ void finish8(const LinearParams& p, const RowOut& r, uint32_t n, float (&v)[8]) {
-  if (p.weight_scale) {
-    const float4* s = reinterpret_cast<const float4*>(p.weight_scale + n);
-    const float4 a = __ldg(s), b = __ldg(s + 1);
-    const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// A row's 32 columns from n on. What they need is requested first (`load`), so that it comes
+// while the sums do; columns past N take the last eight's values and are not stored. The
+// options are decided once for the 32, and the arithmetic runs two elements per instruction:
+// per element it left 22 instructions, which set the pace at small K.
+template <bool FP8, bool FP16>
+struct Columns {
+  uint4 bias[4], gate[4];
+  float4 scale[FP8 ? 8 : 1];
+
+  __device__ __forceinline__ void load(const LinearParams& p, const RowOut& r, uint32_t n) {
+    const uint32_t last = p.N - 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= r.x_scale * w[i];
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t at = min(n + 8 * i, last);
+      if (p.bias) bias[i] = __ldg(reinterpret_cast<const uint4*>(p.bias + at));
+      if (r.gate) gate[i] = __ldg(reinterpret_cast<const uint4*>(r.gate + at));
+      if (FP8) {
+        scale[2 * i] = __ldg(reinterpret_cast<const float4*>(p.weight_scale + at));
+        scale[2 * i + 1] = __ldg(reinterpret_cast<const float4*>(p.weight_scale + at) + 1);
+      }
+    }
   }
-  if (p.bias) {
-    float b[8];
-    widen8<FP16>(__ldg(reinterpret_cast<const uint4*>(p.bias + n)), b);
+  __device__ __forceinline__ static uint64_t pair(const uint4& v, int i) {
+    const float2 e = widen16<FP16>(fused_norm_impl::word(v, i));
+    return fused_norm_impl::pk2(e.x, e.y);
+  }
+  // v: the sums of columns [8 i, 8 i + 8) in its i-th part; e: the residual, packed; out in its place.
+  __device__ __forceinline__ void finish(const LinearParams& p, const RowOut& r, float (&v)[32], uint4 (&e)[4]) const {
+    using namespace fused_norm_impl;
+    uint64_t z[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-  }
-  activate(p.act, v);
-  float g[8], e[8];
-  if (r.gate) widen8<FP16>(__ldg(reinterpret_cast<const uint4*>(r.gate + n)), g);
-  if (r.residual) widen8<FP16>(*reinterpret_cast<const uint4*>(r.residual + n), e);  // may be out itself
+    for (int i = 0; i < 16; ++i) z[i] = pk2(v[2 * i], v[2 * i + 1]);
+    if (FP8) {
+      const uint64_t s = pk2(r.x_scale, r.x_scale);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (r.gate && r.residual) v[i] = fmaf(g[i], v[i], e[i]);
-    else if (r.gate) v[i] *= g[i];
-    else if (r.residual) v[i] += e[i];
+      for (int i = 0; i < 8; ++i) {
+        z[2 * i] = mul2(z[2 * i], mul2(s, pk2(scale[i].x, scale[i].y)));
+        z[2 * i + 1] = mul2(z[2 * i + 1], mul2(s, pk2(scale[i].z, scale[i].w)));
+      }
+    }
+    if (p.bias) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z[i] = add2(z[i], pair(bias[i >> 2], i & 3));
+    }
+    if (p.act != BO_ACT_NONE) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) upk2(z[i], v[2 * i], v[2 * i + 1]);
+      activate(p.act, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z[i] = pk2(v[2 * i], v[2 * i + 1]);
+    }
+    if (r.gate) {
+      if (p.has_residual) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = fma2(pair(gate[i >> 2], i & 3), z[i], pair(e[i >> 2], i & 3));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = mul2(z[i], pair(gate[i >> 2], i & 3));
+      }
+    } else if (p.has_residual) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z[i] = add2(z[i], pair(e[i >> 2], i & 3));
+    }
+    uint32_t o[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float a, b;
+      upk2(z[i], a, b);
+      o[i] = pack16<FP16>(a, b);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
   }
-  *reinterpret_cast<uint4*>(r.out + n) = pack8<FP16>(v);
-}
+};
 
 // ---- many rows ----------------------------------------------------------------------------------
 
 constexpr int kTileM = 128;          // rows of a CTA
 constexpr int kStepBytes = 128;      // of K, per row and stage
 constexpr int kMaxStages = 8;
-constexpr int kMatrixThreads = 192;  // TMA, products, four warps of epilogue
+constexpr int kEpilogueWarps = 8;    // two to each quarter of the rows, each half of the columns
+constexpr int kMatrixThreads = 32 * (2 + kEpilogueWarps);
+constexpr int kBox = 32;             // rows and columns of an output box
+constexpr int kBoxBytes = kBox * kBox * 2;
+constexpr int kBoxes = 4;            // of a warp: two being brought, one worked on, one being stored
+constexpr int kBoxesBytes = kEpilogueWarps * kBoxes * kBoxBytes;
 
 template <int CG, int BN>
 struct MatrixShape {
   static constexpr int kABytes = kTileM * kStepBytes, kBBytes = BN / CG * kStepBytes;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kFit = 200 * 1024 / kStageBytes;
+  static constexpr int kFit = (226 * 1024 - 1024 - kBoxesBytes) / kStageBytes;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kColumns = 2 * BN;  // TMEM: two tiles of sums
-  static constexpr int kShared = kStages * kStageBytes + 1024;  // 1024: alignment of the stages
+  static constexpr int kShared = kStages * kStageBytes + kBoxesBytes + 1024;  // 1024: alignment
 };
 
 struct Tile {
@@ -149,10 +203,12 @@ __device__ int linear_gate_gave_up = 0;  // launches in which a wait ran out (th
 template <int CG, int BN, bool FP8, bool FP16>
 __global__ void __launch_bounds__(kMatrixThreads, 1)
 linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant__ CUtensorMap map_x,
-                  const __grid_constant__ CUtensorMap map_w) {
+                  const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_out,
+                  const __grid_constant__ CUtensorMap map_residual) {
   using S = MatrixShape<CG, BN>;
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], sums_full[2], sums_empty[2];
+  __shared__ __align__(8) uint64_t box_full[kEpilogueWarps][kBoxes];
   __shared__ uint32_t tmem_at;
   __shared__ int failed;
   const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u;
@@ -161,7 +217,8 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) mbar_init(smem_u32(&full[i]), 1), mbar_init(smem_u32(&empty[i]), 1);
-    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sums_full[i]), 1), mbar_init(smem_u32(&sums_empty[i]), 4 * CG);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sums_full[i]), 1), mbar_init(smem_u32(&sums_empty[i]), kEpilogueWarps * CG);
+    for (int i = 0; i < kBoxes * kEpilogueWarps; ++i) mbar_init(smem_u32(&box_full[i / kBoxes][i % kBoxes]), 1);
     failed = 0;
     mbar_init_fence();
   }
@@ -198,10 +255,6 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
         ok = mbar_wait(smem_u32(&empty[stage]), parity ^ 1, &failed);
         if (++stage == S::kStages) stage = 0, parity ^= 1;
       }
-      if (!ok) {  // leave copies in flight the time to land
-        const uint64_t start = now_ns();
-        while (now_ns() - start < 1000000000ull) __nanosleep(1000000);
-      }
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
@@ -226,32 +279,82 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
       }
     }
   } else {
-    const int quarter = warp & 3;  // the TMEM lanes that this warp may read
-    uint32_t n = 0;
-    for (uint32_t t = first; t < p.tiles; t += step, ++n) {
-      const uint32_t buf = n & 1, round = (n >> 1) & 1;
-      if (!mbar_wait(smem_u32(&sums_full[buf]), round, &failed)) break;
+    const int mine = warp - 2, quarter = warp & 3;  // quarter: the TMEM lanes that this warp may read
+    constexpr uint32_t kHalf = BN / 2, kChunks = kHalf / kBox;
+    const uint32_t half = (mine >> 2) * kHalf;           // its columns of a tile
+    const uint32_t boxes = stages + S::kStages * S::kStageBytes + mine * kBoxes * kBoxBytes;
+    const uint32_t bars = smem_u32(&box_full[mine][0]);
+    // The residual boxes of this warp's chunks, brought in order, two ahead; lane 0 only.
+    uint32_t next_t = first, next_c = 0, next_box = 0;
+    auto fetch = [&]() {
+      if (next_t >= p.tiles) return;
+      const Tile at = tile_at(p, next_t);
+      mbar_expect(bars + 8 * next_box, kBoxBytes);
+      tma_load<false>(boxes + next_box * kBoxBytes, &map_residual, (int)(at.n * BN + half + next_c * kBox),
+                      (int)((at.m * CG + rank) * kTileM) + quarter * 32, (int)at.batch, bars + 8 * next_box);
+      next_box = (next_box + 1) % kBoxes;
+      if (++next_c == kChunks) next_c = 0, next_t += step;
+    };
+    if (p.has_residual && lane == 0) fetch(), fetch();
+    uint32_t n = 0, chunk = 0;
+    bool ok = true;
+    for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
+      const uint32_t acc = n & 1, round = (n >> 1) & 1;
+      if (!(ok = mbar_wait(smem_u32(&sums_full[acc]), round, &failed))) break;
       __syncwarp();
       tc_fence_after();
       const Tile at = tile_at(p, t);
-      const uint32_t in_batch = (at.m * CG + rank) * kTileM + quarter * 32 + lane;
-      const bool live = in_batch < p.batch_rows;
-      const RowOut r = row_out(p, live ? at.batch * p.batch_rows + in_batch : 0u);
-      const uint32_t n0 = at.n * BN;
+      const uint32_t row0 = (at.m * CG + rank) * kTileM + quarter * 32;
+      const bool live = row0 + lane < p.batch_rows;
+      const RowOut r = row_out(p, live ? at.batch * p.batch_rows + row0 + lane : 0u);
+      const uint32_t n0 = at.n * BN + half;
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
-        if (n0 + c >= p.N) break;
+      for (uint32_t c = 0; c < kChunks; ++c, ++chunk) {
+        const uint32_t buf = chunk % kBoxes;
+        Columns<FP8, FP16> columns;
+        columns.load(p, r, n0 + c * kBox);
         float v[32];
-        tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN + c, v);
+        tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + half + c * kBox, v);
+        if (lane == 0) {
+          if (p.has_residual) {
+            tma_stores_read<1>();  // of the box two chunks ago: the residual two ahead goes there
+            fetch();
+          } else {
+            tma_stores_read<kBoxes - 1>();  // of this box
+          }
+        }
         tmem_wait();
+        if (c + 1 == kChunks) {  // the sums are in registers: the next tile may have their place
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to(smem_u32(&sums_empty[acc]), 0));
+        }
+        if (p.has_residual && !(ok = mbar_wait(bars + 8 * buf, (chunk / kBoxes) & 1, &failed))) break;
+        __syncwarp();
+        // row `lane` of the box: 64 bytes, 16-byte pieces swizzled as TMA's 64-byte mode has them
+        const uint32_t row = boxes + buf * kBoxBytes + lane * 64;
+        auto piece = [&](int i) { return row + ((i ^ ((lane >> 1) & 3)) << 4); };
+        uint4 e[4];
+        if (p.has_residual) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(e[i].x), "=r"(e[i].y), "=r"(e[i].z), "=r"(e[i].w) : "r"(piece(i)) : "memory");
+        }
+        columns.finish(p, r, v, e);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (live && n0 + c + 8 * i < p.N) finish8<FP16>(p, r, n0 + c + 8 * i, reinterpret_cast<float(&)[8]>(v[8 * i]));
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(piece(i)), "r"(e[i].x), "r"(e[i].y), "r"(e[i].z), "r"(e[i].w) : "memory");
+        fence_for_tma();
+        __syncwarp();
+        if (lane == 0 && row0 < p.batch_rows && n0 + c * kBox < p.N)
+          tma_store(&map_out, boxes + buf * kBoxBytes, (int)(n0 + c * kBox), (int)row0, (int)at.batch);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_to(smem_u32(&sums_empty[buf]), 0));
     }
+    if (lane == 0) tma_stores_done();
+  }
+  if (failed && threadIdx.x % 32 == 0) {  // leave copies in flight the time to land
+    const uint64_t start = now_ns();
+    while (now_ns() - start < 1000000000ull) __nanosleep(1000000);
   }
   __syncwarp();
   tc_fence_before();
@@ -345,10 +448,11 @@ __global__ void __launch_bounds__(kTokenThreads) linear_gate_tokens(const __grid
   float a[1] = {v};
   activate(p.act, a);
   v = a[0];
-  if (r.gate && r.residual) v = fmaf(one(r.gate + n), v, one(r.residual + n));
+  const uint16_t* e = p.residual.ptr + (r.b * p.residual.sb + r.l * p.residual.sl) + n;
+  if (r.gate && p.has_residual) v = fmaf(one(r.gate + n), v, one(e));
   else if (r.gate) v *= one(r.gate + n);
-  else if (r.residual) v += one(r.residual + n);
-  r.out[n] = (uint16_t)pack16<FP16>(v, 0.0f);
+  else if (p.has_residual) v += one(e);
+  p.out[r.b * p.out_sb + r.l * p.out_sl + n] = (uint16_t)pack16<FP16>(v, 0.0f);
 }
 
 }  // namespace block_ops

@@ -96,6 +96,22 @@ __device__ __forceinline__ void tma_load(uint32_t to, const CUtensorMap* m, int 
         : "memory");
 }
 
+// A box of this CTA's shared memory to a 3-d map (what lies outside the tensor is left out), and
+// the waits for the thread's own stores: read (the buffer may be written again) and done.
+__device__ __forceinline__ void tma_store(const CUtensorMap* m, uint32_t from, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m), "r"(x), "r"(y),
+               "r"(z), "r"(from)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void tma_stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// This thread's writes to shared memory before TMA's reads of it.
+__device__ __forceinline__ void fence_for_tma() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // ---- tcgen05 ------------------------------------------------------------------------------------
 
 template <int CG>
