@@ -1,19 +1,13 @@
-"""ctypes view of include/block_ops.h (argument marshalling only; the library is the one of
-``_abi``, and loading it fails loudly when it has not been built)."""
+"""ctypes view of include/block_ops.h, and the extension behind the package's tensor-level
+functions. The library is the one of ``_abi``; loading either fails loudly when it has not been
+built."""
 from __future__ import annotations
 
 import ctypes
-import threading
-from typing import Dict, Tuple
-
-import torch
-
 from . import _abi
 from ._abi import fn_operand
 
 BO_BF16, BO_FP16, BO_E4M3, BO_FP32 = 0, 1, 2, 3
-DTYPE_CODES = {torch.bfloat16: BO_BF16, torch.float16: BO_FP16, torch.float8_e4m3fn: BO_E4M3,
-               torch.float32: BO_FP32}
 
 _int, _i64, _ptr, _dbl = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_double
 
@@ -118,36 +112,18 @@ def check(status: int, what: str) -> None:
     raise _abi.FusedNormError(status, what, detail)
 
 
-_handles: Dict[Tuple, int] = {}
-_handles_lock = threading.Lock()
+_binding = None
 
 
-def handle(op: str, key: Tuple, make_config) -> int:
-    """The operator's handle for a configuration, created once per process."""
-    key = (op,) + key
-    h = _handles.get(key)
-    if h is None:
-        with _handles_lock:
-            h = _handles.get(key)
-            if h is None:
-                cfg, out = make_config(), ctypes.c_void_p()
-                check(getattr(load(), f"{op}_create")(ctypes.byref(out), ctypes.byref(cfg)), f"{op}_create")
-                h = _handles[key] = out.value
-    return h
-
-
-def rope_norm_workspace(h: int, B: int, L: int) -> int:
-    """Bytes of workspace of a backward launch."""
-    n = ctypes.c_uint64()
-    check(load().rope_norm_backward_workspace(h, B, L, ctypes.byref(n)), "rope_norm_backward_workspace")
-    return n.value
-
-
-def launch(op: str, h: int, args, device: torch.device, stream, call: str = "launch") -> None:
-    """One call on `stream` (default: the current stream of `device`), with `device` current
-    for it."""
-    with torch.cuda.device(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        status = getattr(load(), f"{op}_{call}")(h, ctypes.byref(args), int(stream.cuda_stream))
-    check(status, f"{op}_{call}")
+def binding():
+    """The extension behind norm_quant, rope and linear (csrc/binding)."""
+    global _binding
+    if _binding is None:
+        _abi.load()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise ImportError("rmsnorm_row_b200/_binding.so does not load: build it with `python -m rmsnorm_row_b200.build` "
+                              f"(there is no fallback implementation): {e}") from e
+        _binding = module
+    return _binding

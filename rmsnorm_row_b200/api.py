@@ -55,22 +55,22 @@ def _handle(D: int, is_rms: bool, has_gate: bool, has_weight: bool, has_bias: bo
         return h
 
 
-def _check_tensor(t: torch.Tensor, name: str, device: torch.device, dtype: torch.dtype = torch.bfloat16) -> None:
+def _check_tensor(t: torch.Tensor, name: str, device: torch.device) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {str(dtype).removeprefix('torch.')}, got {t.dtype}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dim() >= 1 and t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} needs a contiguous channel dimension")
 
 
-def _operand(t: Optional[torch.Tensor], name: str, B: int, L: int, D: int, device, dtype: torch.dtype = torch.bfloat16):
+def _operand(t: Optional[torch.Tensor], name: str, B: int, L: int, D: int, device):
     """(fn_operand, frames) for a gate/scale/shift tensor; frames is 0 without a frame axis."""
     if t is None:
         return _abi.fn_operand(None, 0, 0, 0), 0
-    _check_tensor(t, name, device, dtype)
+    _check_tensor(t, name, device)
     if t.shape[-1] != D:
         raise ValueError(f"{name} has {t.shape[-1]} channels, expected {D}")
     s = t.stride()

@@ -7,6 +7,9 @@ Each .cu under csrc/ and csrc/block/ compiles on its own (in parallel) with
 library with the CUDA runtime linked statically, so loading the library needs no
 GPU and no CUDA shared libraries beyond the driver at launch time.
 Precise division and square root are kept (no fast-math).
+
+csrc/binding/ is the Python side of the operators of include/block_ops.h, a CPython extension
+(_binding.so) against the installed PyTorch that links to the library.
 """
 from __future__ import annotations
 
@@ -21,6 +24,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libfused_norm.so")
+BINDING = os.path.join(HERE, "_binding.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -48,10 +52,31 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _build_binding() -> None:
+    import sysconfig
+
+    import torch
+
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    root = os.path.dirname(torch.__file__)
+    includes = [sysconfig.get_paths()["include"], os.path.join(root, "include"), os.path.join(cuda, "include")]
+    libs = os.path.join(root, "lib")
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f for d in includes for f in ("-isystem", d)), os.path.join(CSRC, "binding", "block_ops.cpp"),
+           "-o", tmp, LIB, "-L" + libs, "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"the binding does not compile:\n{res.stderr[-4000:]}")
+    os.replace(tmp, BINDING)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     srcs = glob.glob(os.path.join(CSRC, "**", "*"), recursive=True) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
     return any(os.path.getmtime(s) > t for s in srcs)
 
@@ -64,9 +89,10 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int = 4) -> st
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
     tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
+    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp, *objs]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    _build_binding()
     return LIB
 
 
