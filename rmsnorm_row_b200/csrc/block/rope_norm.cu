@@ -30,25 +30,61 @@ __global__ void __launch_bounds__(256) sum_partials(const float* partial, int pa
 
 struct RopeShape {
   int W, T, G, nh, rows_per_cta;
+  RopeKernel kernel;
+  size_t smem;
+  int stages;
 };
+constexpr size_t kMaxShared = 227 * 1024;  // of a CTA
 
-// Lanes of a head, threads of a row and heads of a thread. Rows of more than 32 lanes take the
-// number of heads per thread (1, 2 or 4) that leaves the fewest idle lanes, 2 where it is even.
-RopeShape rope_shape(int H, int hd) {
-  RopeShape s;
-  s.W = 1;
-  while (s.W < hd / 16) s.W *= 2;
-  if (H * s.W <= 32) {
-    s.nh = 1, s.T = 1;
-    while (s.T < H * s.W) s.T *= 2;
-  } else {
-    s.T = 0;
-    for (int nh : {2, 1, 4}) {
-      const int T = ((H + nh - 1) / nh * s.W + 31) / 32 * 32;
-      if (T <= kRopeThreads && (s.T == 0 || T * nh < s.T * s.nh)) s.T = T, s.nh = nh;
+int lanes_of(int hd) {
+  int W = 1;
+  while (W < hd / 16) W *= 2;
+  return W;
+}
+RopeShape shared_warps(int H, int W) {  // a row of up to 32 lanes
+  int T = 1;
+  while (T < H * W) T *= 2;
+  return RopeShape{W, T, T / W, 1, kSharedRows / T, nullptr, 0, 0};
+}
+
+// Forward: a warp to a row where a lane can hold its part of it (10 heads, 80 registers), or in
+// the case of a norm that is not over all heads, in passes of four; CTAs of several warps for
+// longer rows. With `few` rows, the warps of a CTA share a row two heads to a lane; both add up
+// squares in the same order.
+RopeShape forward_shape(int H, int hd, int norm, bool few) {
+  const int W = lanes_of(hd), G = 32 / W, need = (H + G - 1) / G;
+  if (H * W <= 32) return shared_warps(H, W);
+  RopeShape s{W, 32, G, 2, kSharedRows / 32, nullptr, 0, 0};
+  int P = 1;
+  if (norm == BO_NORM_ALL && need > 10) {
+    P = 0;
+    for (int nh : {10, 6, 4}) {
+      const int n = (need + nh - 1) / nh;
+      if (P == 0 || (n <= kForwardThreads / 32 && n * nh < P * s.nh)) P = n, s.nh = nh;
     }
+  } else if (few) {
+    P = (need + 1) / 2 < kForwardThreads / 32 ? (need + 1) / 2 : kForwardThreads / 32;
+  } else if (norm == BO_NORM_ALL) {
+    s.nh = need <= 2 ? 2 : need <= 4 ? 4 : need <= 6 ? 6 : 10;
+  } else {
+    s.nh = need <= 2 ? 2 : 4;
   }
-  s.G = s.T / s.W;
+  s.T = 32 * P;
+  if (P > 1) s.rows_per_cta = 1;
+  return s;
+}
+
+// Gradient: rows of more than 32 lanes take the number of heads per thread (1, 2 or 4) that
+// leaves the fewest idle lanes, 2 where it is even.
+RopeShape backward_shape(int H, int hd) {
+  const int W = lanes_of(hd);
+  if (H * W <= 32) return shared_warps(H, W);
+  RopeShape s{W, 0, 0, 0, 0, nullptr, 0, 0};
+  for (int nh : {2, 1, 4}) {
+    const int T = ((H + nh - 1) / nh * W + 31) / 32 * 32;
+    if (T <= (nh == 4 ? kRopeThreads : kGradientThreads) && (s.T == 0 || T * nh < s.T * s.nh)) s.T = T, s.nh = nh;
+  }
+  s.G = s.T / W;
   s.rows_per_cta = s.T > 32 ? 1 : kSharedRows / s.T;
   return s;
 }
@@ -60,16 +96,16 @@ using namespace block_ops;
 
 struct rope_norm_s {
   rn_config cfg;
-  RopeShape shape;
-  RopeKernel forward, backward;
+  RopeShape shape[3];  // kForward, kFew, kGradient
   RopeParams base;  // the parts of the launch parameters that the configuration settles
-  size_t smem[2];  // of the two kernels
-  mutable std::atomic<int> resident[2] = {{0}, {0}};  // CTAs per SM of the two kernels, once known
+  mutable std::atomic<int> resident[3] = {{0}, {0}, {0}};  // CTAs per SM of the kernels, once known
 };
 
 namespace {
 
 int weight_values(const rn_config& c) { return c.norm == BO_NORM_ALL ? c.heads * c.head_dim : c.head_dim; }
+enum { kForward = 0, kFew = 1, kGradient = 2 };
+constexpr int kFewPerSm = 4;  // rows
 bool sums_dweight(const rn_config& c) { return c.has_weight != 0; }
 
 bool rows_extent(const rn_rows& r, int64_t B, int64_t L, const rn_config& c, Span* out) {
@@ -164,11 +200,11 @@ fn_status validate(const rope_norm_s* h, const rn_args* a, bool* empty) {
   return check(h, a->B, a->L, ins, a->y, a->positions, a->pos_stride_b, a->pos_stride_l, a->weight, Span{}, Span{});
 }
 
-int64_t ctas(const rope_norm_s* h, int64_t rows) { return (rows + h->shape.rows_per_cta - 1) / h->shape.rows_per_cta; }
+int64_t ctas(const RopeShape& s, int64_t rows) { return (rows + s.rows_per_cta - 1) / s.rows_per_cta; }
 
 uint64_t workspace_bytes(const rope_norm_s* h, int64_t rows) {
   if (!sums_dweight(h->cfg) || rows == 0) return 0;
-  const int64_t n = ctas(h, rows);
+  const int64_t n = ctas(h->shape[kGradient], rows);
   return (uint64_t)(n < kMaxPartials ? n : kMaxPartials) * weight_values(h->cfg) * sizeof(float);
 }
 
@@ -194,48 +230,67 @@ RopeRows rows_of(const rn_rows& r) {
 }
 
 // Above 48 KB a kernel's shared memory is asked for, once per device context.
-cudaError_t allow_shared(const rope_norm_s* h, bool back) {
-  if (h->smem[back] <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(back ? h->backward : h->forward, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)h->smem[back]);
+cudaError_t allow_shared(const RopeShape& s) {
+  if (s.smem <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(s.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
+}
+
+fn_status sms_of(int* sms) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, device);
+  return e == cudaSuccess ? FN_OK : launch_status(e);
 }
 
 // The number of CTAs: what the current device holds at once, at most one per rows_per_cta rows.
-fn_status grid_of(const rope_norm_s* h, bool back, int64_t rows, int* grid) {
-  int per_sm = h->resident[back].load(std::memory_order_relaxed);
+fn_status grid_of(const rope_norm_s* h, int which, int64_t rows, int sms, int* grid) {
+  const RopeShape& s = h->shape[which];
+  int per_sm = h->resident[which].load(std::memory_order_relaxed);
   if (per_sm == 0) {
-    cudaError_t e = allow_shared(h, back);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-        &per_sm, back ? h->backward : h->forward, h->shape.T * h->shape.rows_per_cta, h->smem[back]);
+    cudaError_t e = allow_shared(s);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, s.kernel, s.T * s.rows_per_cta, s.smem);
     if (e != cudaSuccess) return launch_status(e);
     if (per_sm < 1) per_sm = 1;
-    h->resident[back].store(per_sm, std::memory_order_relaxed);
+    h->resident[which].store(per_sm, std::memory_order_relaxed);
   }
-  int device = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
-  if (e != cudaSuccess) return launch_status(e);
   int64_t g = (int64_t)per_sm * sms;
-  if (back && sums_dweight(h->cfg) && g > kMaxPartials) g = kMaxPartials;
-  const int64_t n = ctas(h, rows);
+  if (which == kGradient && g > kMaxPartials) g = kMaxPartials;
+  const int64_t n = ctas(s, rows);
   *grid = (int)(g < n ? g : n);
   return FN_OK;
 }
 
-fn_status run(const rope_norm_s* h, bool back, int grid, RopeParams& p, int64_t B, int64_t L, const void* positions, int64_t psb,
-              int64_t psl, const void* weight, const rn_rows& out, cudaStream_t stream) {
+fn_status run(const rope_norm_s* h, int which, RopeParams& p, int64_t B, int64_t L, const void* positions, int64_t psb,
+              int64_t psl, const void* weight, const rn_rows& out, int sms, cudaStream_t stream, int* grid) {
+  const RopeShape& s = h->shape[which];
+  fn_status st = grid_of(h, which, B * L, sms, grid);
+  if (st != FN_OK) return st;
+  p.W = s.W, p.T = s.T, p.G = s.G, p.stages = s.stages;
   p.out = rows_of(out);
   p.positions = positions, p.pos_sb = psb, p.pos_sl = psl;
   p.weight = weight;
   p.rows = (uint32_t)(B * L), p.L = (uint32_t)L;
   p.div_L = fused_norm_impl::make_div_u32(p.L);
-  const cudaError_t e = allow_shared(h, back);
+  const cudaError_t e = allow_shared(s);
   if (e != cudaSuccess) return launch_status(e);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(h->shape.T * h->shape.rows_per_cta);
-  cfg.dynamicSmemBytes = h->smem[back];
+  cfg.gridDim = dim3(*grid);
+  cfg.blockDim = dim3(s.T * s.rows_per_cta);
+  cfg.dynamicSmemBytes = s.smem;
   cfg.stream = stream;
-  return launch_status(cudaLaunchKernelEx(&cfg, back ? h->backward : h->forward, p));
+  return launch_status(cudaLaunchKernelEx(&cfg, s.kernel, p));
+}
+
+// The forward kernel over x, which also turns a gradient back (SIGN -1) where there is no norm.
+fn_status run_forward(const rope_norm_s* h, const rn_rows& x, float sign, int64_t B, int64_t L, const void* positions, int64_t psb,
+                      int64_t psl, const void* weight, const rn_rows& out, cudaStream_t stream) {
+  int sms, grid;
+  const fn_status s = sms_of(&sms);
+  if (s != FN_OK) return s;
+  RopeParams p = h->base;
+  p.x = rows_of(x);
+  p.sign = sign;
+  return run(h, B * L <= (int64_t)kFewPerSm * sms ? kFew : kForward, p, B, L, positions, psb, psl, weight, out, sms, stream, &grid);
 }
 
 }  // namespace
@@ -264,20 +319,30 @@ fn_status rope_norm_create(rope_norm_t* out, const rn_config* cfg) {
   rope_norm_s* h = new (std::nothrow) rope_norm_s;
   if (!h) return FN_ERR_INVALID_ARG;
   h->cfg = c;
-  const RopeShape s = h->shape = rope_shape(c.heads, c.head_dim);
-  auto pick = [&](bool back) {
-    return c.dtype == BO_FP16 ? pick_rope<true>(s.nh, c.norm, c.half_pairs, back, back && sums_dweight(c))
-                              : pick_rope<false>(s.nh, c.norm, c.half_pairs, back, back && sums_dweight(c));
-  };
-  h->forward = pick(false), h->backward = pick(true);
-  for (int back = 0; back < 2; ++back)
-    h->smem[back] = rope_shared_bytes(s.rows_per_cta, (int)pairs, s.T * s.rows_per_cta, s.nh, back != 0);
+  const int units = c.has_weight ? weight_values(c) / 16 : 0, weights = weight_floats(units);
+  for (int i : {kForward, kFew, kGradient}) {
+    RopeShape& s = h->shape[i];
+    s = i == kGradient ? backward_shape(c.heads, c.head_dim) : forward_shape(c.heads, c.head_dim, c.norm, i == kFew);
+    if (i != kGradient) {
+      s.kernel = c.dtype == BO_FP16 ? pick_rope<true>(s.nh, c.norm, c.half_pairs) : pick_rope<false>(s.nh, c.norm, c.half_pairs);
+      s.smem = forward_shared_bytes(s.rows_per_cta, c.head_dim, weights);
+    } else if (c.norm != BO_NORM_NONE) {
+      s.kernel = c.dtype == BO_FP16 ? pick_rope_gradient<true>(s.nh, c.norm, c.half_pairs, sums_dweight(c))
+                                    : pick_rope_gradient<false>(s.nh, c.norm, c.half_pairs, sums_dweight(c));
+      for (s.stages = kStages; s.stages >= 1; --s.stages) {
+        s.smem = backward_shared_bytes(s.rows_per_cta, c.head_dim, weights, s.T * s.rows_per_cta, s.nh, s.stages);
+        if (s.smem <= kMaxShared) break;
+      }
+    }
+  }
   RopeParams& p = h->base;
   std::memset(&p, 0, sizeof(p));
   p.H = c.heads, p.hd = c.head_dim, p.units = c.head_dim / 16, p.pairs = (int)pairs;
-  p.W = s.W, p.T = s.T, p.G = s.G;
+  p.passes = 2 * pairs < c.head_dim;
+  p.sign = 1.0f;
   p.index64 = c.index64, p.weight_fp32 = c.weight_fp32;
-  p.weight_sh = c.norm == BO_NORM_ALL ? c.head_dim : 0;
+  p.weight_sh = c.norm == BO_NORM_ALL ? c.head_dim / 16 : 0;
+  p.weight_units = units;
   p.inv_n64 = 1.0 / (c.norm == BO_NORM_ALL ? c.heads * c.head_dim : c.head_dim), p.eps64 = c.eps;
   p.inv_n = (float)p.inv_n64, p.eps = (float)c.eps;
   int i = 0;
@@ -298,15 +363,10 @@ fn_status rope_norm_validate(rope_norm_t h, const rn_args* a) {
 
 fn_status rope_norm_launch(rope_norm_t h, const rn_args* a, fn_stream_t stream) {
   bool empty;
-  fn_status s = validate(h, a, &empty);
+  const fn_status s = validate(h, a, &empty);
   if (s != FN_OK || empty) return s;
-  int grid;
-  s = grid_of(h, false, a->B * a->L, &grid);
-  if (s != FN_OK) return s;
-  RopeParams p = h->base;
-  p.x = rows_of(a->x);
-  return run(h, false, grid, p, a->B, a->L, a->positions, a->pos_stride_b, a->pos_stride_l, a->weight, a->y,
-             reinterpret_cast<cudaStream_t>(stream));
+  return run_forward(h, a->x, 1.0f, a->B, a->L, a->positions, a->pos_stride_b, a->pos_stride_l, a->weight, a->y,
+                     reinterpret_cast<cudaStream_t>(stream));
 }
 
 fn_status rope_norm_backward_workspace(rope_norm_t h, int64_t B, int64_t L, uint64_t* bytes) {
@@ -330,13 +390,15 @@ fn_status rope_norm_backward_launch(rope_norm_t h, const rn_backward_args* a, fn
   const int n = weight_values(h->cfg);
   if (empty)
     return a->dweight ? launch_status(cudaMemsetAsync(a->dweight, 0, (size_t)n * 4, stream)) : FN_OK;
-  int grid;
-  s = grid_of(h, true, a->B * a->L, &grid);
+  if (h->cfg.norm == BO_NORM_NONE)
+    return run_forward(h, a->grad, -1.0f, a->B, a->L, a->positions, a->pos_stride_b, a->pos_stride_l, nullptr, a->dx, stream);
+  int sms, grid;
+  s = sms_of(&sms);
   if (s != FN_OK) return s;
   RopeParams p = h->base;
   p.x = rows_of(a->x), p.dy = rows_of(a->grad);
   p.partial = static_cast<float*>(a->workspace);
-  s = run(h, true, grid, p, a->B, a->L, a->positions, a->pos_stride_b, a->pos_stride_l, a->weight, a->dx, stream);
+  s = run(h, kGradient, p, a->B, a->L, a->positions, a->pos_stride_b, a->pos_stride_l, a->weight, a->dx, sms, stream, &grid);
   if (s != FN_OK || !a->dweight) return s;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((n + 31) / 32);

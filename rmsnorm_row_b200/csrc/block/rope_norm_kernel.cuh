@@ -6,19 +6,17 @@
 // The gradient turns grad back (dn), then dx = rho (w dn - x rho^2 mean(w dn x)) and
 // dw = sum dn x rho.
 //
-// Bound: HBM. A token moves 2 + 2 bytes per channel (gradient: 2 + 2 + 2) against ~10 fp32
-// operations (~25). The angle of a pair is shared by all heads of a token: one thread reduces
-// it in fp64 and leaves cos and sin in shared memory, one token ahead of its use.
+// Bound: HBM. A token moves 2 + 2 bytes per channel (gradient: 2 + 2 + 2). At the copy rate an
+// SM has about 3500 instruction slots for a forward row of 5120 channels and 5200 for a gradient
+// row, so instructions count too: the arithmetic runs on pairs of fp32, a warp keeps a whole
+// row, and the angles of a token, which all heads share, are reduced once (in fp64) and left
+// as cos and sin in shared memory.
 //
 // Layout: a thread owns "units" of 16 channels of a head as two 16-byte vectors A and B, the
-// same unit u in each of its heads h = g, g + G, ... (g: its lane group of W lanes, W the
-// power of two from hd / 16 up). Half pairing puts the 8 partners of A in B, so every pair is
-// inside one thread; adjacent pairing has A in the head's first half and B in its second, so
-// that neighbouring lanes touch neighbouring vectors. A norm over the head is a shuffle inside
-// W lanes. Rows of up to 32 lanes share warps; longer rows are a CTA with one barrier per
-// token. CTAs are persistent; each thread copies its own vectors of the
-// next two tokens to shared memory while it works on the present one, so no registers wait
-// for loads and nobody else has to be waited for.
+// same unit u in each of its heads (W lanes to a head, W the power of two from hd / 16 up).
+// Half pairing puts the 8 partners of A in B, so every pair is inside one thread; adjacent
+// pairing has A in the head's first half and B in its second, so that neighbouring lanes touch
+// neighbouring vectors. A norm over the head is a shuffle inside W lanes.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -36,7 +34,9 @@ using fused_norm_impl::div_u32;
 
 constexpr int kMaxPairs = 256;      // of a head
 constexpr int kRopeThreads = 512;   // of a CTA, at most
+constexpr int kForwardThreads = 384;  // of a forward CTA: 168 registers hold a lane's ten heads
 constexpr int kSharedRows = 128;    // threads of a CTA whose rows take 32 lanes or fewer
+constexpr int kGradientThreads = 384; // of a gradient CTA with one or two heads to a thread
 constexpr int kMaxPartials = 1024;  // CTAs that sum dweight
 
 struct RopeRows {
@@ -54,8 +54,12 @@ struct RopeParams {
   uint32_t rows, L;
   DivU32 div_L;
   int H, hd, units, pairs;  // units of a head (hd / 16), pairs that turn
-  int W, T, G;              // lanes of a head, threads of a row, T / W
-  int index64, weight_fp32, weight_sh;  // weight's step from head to head (0: one head's)
+  int W, T, G;              // lanes of a head, threads of a row, lane groups (of a warp, in the forward kernel)
+  int passes;               // some pairs of a head do not turn
+  int stages;               // rows of the gradient kernel in shared memory: 1 to 3
+  float sign;               // -1 turns the other way
+  int index64, weight_fp32;
+  int weight_sh, weight_units;  // units from a head's weights to the next (0: one head's); units of it (0: none)
   float inv_n, eps;
   double inv_n64, eps64;
   double turns[kMaxPairs];    // freq / 2 pi
@@ -100,68 +104,168 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack16<FP16>(f[6], f[7]));
 }
 
-template <bool FP16>
-__device__ __forceinline__ void load_weight8(const void* w, bool fp32, int at, float (&f)[8]) {
-  if (fp32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
-    const float4 a = __ldg(q), b = __ldg(q + 1);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  } else {
-    widen8<FP16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + at)), f);
-  }
-}
-
 // ---- one thread's place in a row ---------------------------------------------------------------
 
 struct Place {
   int u, g;        // unit, lane group
   int offA, offB;  // channels of the two vectors in the head
+  int pairA, pairB;  // first pairs of the two runs of four that the thread turns
   bool owns;       // u is a unit of the head
 };
 
 template <bool HALF>
-__device__ __forceinline__ Place place_of(const RopeParams& p, int t) {
+__device__ __forceinline__ Place unit_place(const RopeParams& p, int u) {
   Place q;
-  q.u = t & (p.W - 1);
-  q.g = t / p.W;
-  q.owns = q.u < p.units;
+  q.u = u, q.g = 0, q.owns = true;
   if (!HALF) {
     q.offA = 8 * q.u, q.offB = p.hd / 2 + 8 * q.u;
-  } else if (8 * q.u < p.pairs) {
-    q.offA = 8 * q.u, q.offB = p.pairs + 8 * q.u;
+    q.pairA = 4 * q.u, q.pairB = p.hd / 4 + 4 * q.u;
   } else {
-    q.offA = 16 * q.u, q.offB = 16 * q.u + 8;  // channels that pass
+    q.offA = 8 * q.u, q.offB = p.pairs + 8 * q.u;
+    if (8 * q.u >= p.pairs) q.offA = 16 * q.u, q.offB = 16 * q.u + 8;  // channels that pass
+    q.pairA = 8 * q.u, q.pairB = 8 * q.u + 4;
   }
   return q;
 }
+// Thread t's unit and head group.
+template <bool HALF>
+__device__ __forceinline__ Place place_of(const RopeParams& p, int t) {
+  const int u = t & (p.W - 1);
+  Place q = unit_place<HALF>(p, u < p.units ? u : 0);  // without a unit it reads what it may, and stores nothing
+  q.g = t / p.W;
+  q.owns = u < p.units;
+  return q;
+}
 
-// The pairs of a unit turned by (cos, sin) from the table of this row; SIGN -1 turns back.
-template <bool HALF, int SIGN>
-__device__ __forceinline__ void turn(const RopeParams& p, const Place& q, const float2* cs, float (&a)[8], float (&b)[8]) {
-  if (HALF) {
-    if (8 * q.u >= p.pairs) return;
+// The unit's 16 values as fp32 pairs {first, second}[4]: element j of each holds two pairs'
+// first (second) channels, so that one instruction works on two pairs. The four words of
+// adjacent pairing hold a pair each; those of half pairing hold two pairs' same side.
+template <bool FP16, bool HALF>
+__device__ __forceinline__ void split(const uint4& a, const uint4& b, uint64_t (&first)[4], uint64_t (&second)[4]) {
+  using namespace fused_norm_impl;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 e = cs[8 * q.u + i];
-      const float s = SIGN * e.y, y0 = fmaf(a[i], e.x, -b[i] * s);
-      b[i] = fmaf(a[i], s, b[i] * e.x);
-      a[i] = y0;
-    }
-  } else {
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      float(&v)[8] = side ? b : a;
-      const int first = side ? p.hd / 4 + 4 * q.u : 4 * q.u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (first + i >= p.pairs) continue;
-        const float2 e = cs[first + i];
-        const float s = SIGN * e.y, y0 = fmaf(v[2 * i], e.x, -v[2 * i + 1] * s);
-        v[2 * i + 1] = fmaf(v[2 * i], s, v[2 * i + 1] * e.x);
-        v[2 * i] = y0;
-      }
+  for (int j = 0; j < 4; ++j) {
+    if (HALF) {
+      const float2 e = widen16<FP16>(word(a, j)), f = widen16<FP16>(word(b, j));
+      first[j] = pk2(e.x, e.y), second[j] = pk2(f.x, f.y);
+    } else {
+      const uint4& v = j < 2 ? a : b;
+      const float2 e = widen16<FP16>(word(v, 2 * (j & 1))), f = widen16<FP16>(word(v, 2 * (j & 1) + 1));
+      first[j] = pk2(e.x, f.x), second[j] = pk2(e.y, f.y);
     }
   }
+}
+template <bool FP16, bool HALF>
+__device__ __forceinline__ void join(const uint64_t (&first)[4], const uint64_t (&second)[4], uint4& a, uint4& b) {
+  uint32_t wa[4], wb[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float x0, x1, y0, y1;
+    fused_norm_impl::upk2(first[j], x0, x1);
+    fused_norm_impl::upk2(second[j], y0, y1);
+    if (HALF) {
+      wa[j] = pack16<FP16>(x0, x1), wb[j] = pack16<FP16>(y0, y1);
+    } else {
+      uint32_t(&w)[4] = j < 2 ? wa : wb;
+      w[2 * (j & 1)] = pack16<FP16>(x0, y0), w[2 * (j & 1) + 1] = pack16<FP16>(x1, y1);
+    }
+  }
+  a = make_uint4(wa[0], wa[1], wa[2], wa[3]), b = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+}
+// Where element (j, half, side) of a split unit lies: channel of the head.
+template <bool HALF>
+__device__ __forceinline__ int channel_of(const Place& q, int j, int half, int side) {
+  if (HALF) return (side ? q.offB : q.offA) + 2 * j + half;
+  return (j < 2 ? q.offA : q.offB) + 4 * (j & 1) + 2 * half + side;
+}
+
+// The weights in shared memory as fp32 in the order of split units, which CTAs keep for all
+// their rows (widening and addressing them in global memory took a fifth of a row's
+// instructions). The four quarters of eight units' values alternate, so that eight lanes read
+// 128 bytes without bank conflicts.
+__host__ __device__ constexpr int weight_floats(int units) { return (units + 7) / 8 * 128; }
+__device__ __forceinline__ int weight_at(int unit) { return (unit >> 3) * 128 + (unit & 7) * 4; }
+
+template <bool FP16, bool HALF>
+__device__ __forceinline__ void fill_weights(const RopeParams& p, float* to) {
+  for (int i = threadIdx.x; i < p.weight_units; i += blockDim.x) {
+    const int h = i / p.units;
+    const Place q = unit_place<HALF>(p, i - h * p.units);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int at = h * p.hd + channel_of<HALF>(q, e / 2 % 4, e & 1, e / 8);
+      to[weight_at(i) + e / 4 * 32 + e % 4] = p.weight_fp32 ? __ldg(static_cast<const float*>(p.weight) + at)
+                                                          : widen16<FP16>(__ldg(static_cast<const uint16_t*>(p.weight) + at)).x;
+    }
+  }
+}
+// x times the weights at w.
+__device__ __forceinline__ void weigh(const float* w, uint64_t (&first)[4], uint64_t (&second)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; j += 2) {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(w + 16 * j), b = *reinterpret_cast<const ulonglong2*>(w + 64 + 16 * j);
+    first[j] = fused_norm_impl::mul2(first[j], a.x), first[j + 1] = fused_norm_impl::mul2(first[j + 1], a.y);
+    second[j] = fused_norm_impl::mul2(second[j], b.x), second[j + 1] = fused_norm_impl::mul2(second[j + 1], b.y);
+  }
+}
+
+// The same value, which the compiler cannot trace: what depends on it is computed where it is
+// used, and not earlier into registers that then wait (addresses of ten heads for all rows, or
+// a row widened for its sum and kept for its output, took more registers than the row).
+__device__ __forceinline__ uint4 here(uint4 v) {
+  asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w));
+  return v;
+}
+template <typename V>
+__device__ __forceinline__ V here(V v) {
+  if constexpr (sizeof(V) == 8) asm volatile("" : "+l"(v));
+  else asm volatile("" : "+r"(v));
+  return v;
+}
+
+// cos and sin of the unit's eight pairs, in the order of a split unit.
+struct Turn {
+  uint64_t c[4], s[4];
+};
+// A row's table: cos of every pair of the head, then sin (1 and 0 for pairs that pass).
+__device__ __forceinline__ Turn load_turn(const RopeParams& p, const Place& q, const float* table) {
+  Turn t;
+  const float* sides[2] = {table, table + p.hd / 2};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint64_t(&o)[4] = i ? t.s : t.c;
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(sides[i] + q.pairA), b = *reinterpret_cast<const ulonglong2*>(sides[i] + q.pairB);
+    o[0] = a.x, o[1] = a.y, o[2] = b.x, o[3] = b.y;
+  }
+  return t;
+}
+__device__ __forceinline__ uint64_t negated(uint64_t v) { return v ^ 0x8000000080000000ull; }
+
+// The pairs turned by their angles (SIGN -1: turned back). Pairs that pass (only where the
+// configuration has some) are put back, or a NaN would enter its partner.
+template <bool HALF, int SIGN>
+__device__ __forceinline__ void turn(const RopeParams& p, const Place& q, const Turn& t, uint64_t (&first)[4], uint64_t (&second)[4]) {
+  using namespace fused_norm_impl;
+  uint64_t x[4], y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t n = negated(t.s[j]);
+    x[j] = fma2(second[j], SIGN > 0 ? n : t.s[j], mul2(first[j], t.c[j]));
+    y[j] = fma2(first[j], SIGN > 0 ? t.s[j] : n, mul2(second[j], t.c[j]));
+  }
+  if (p.passes) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int pair = (j < 2 ? q.pairA : q.pairB) + 2 * (j & 1);
+      float x0, x1, y0, y1, a0, a1, b0, b1;
+      upk2(first[j], x0, x1), upk2(second[j], y0, y1), upk2(x[j], a0, a1), upk2(y[j], b0, b1);
+      if (pair >= p.pairs) a0 = x0, b0 = y0;
+      if (pair + 1 >= p.pairs) a1 = x1, b1 = y1;
+      x[j] = pk2(a0, a1), y[j] = pk2(b0, b1);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) first[j] = x[j], second[j] = y[j];
 }
 
 // Puts back the packed pairs that do not turn.
@@ -171,7 +275,7 @@ __device__ __forceinline__ void keep_passing(const RopeParams& p, const Place& q
     if (8 * q.u >= p.pairs) oa = a, ob = b;
     return;
   }
-  const int ka = p.pairs - 4 * q.u, kb = ka - p.hd / 4;  // pairs of each vector that turn
+  const int ka = p.pairs - q.pairA, kb = p.pairs - q.pairB;  // pairs of each vector that turn
   if (ka < 4) oa = make_uint4(ka > 0 ? oa.x : a.x, ka > 1 ? oa.y : a.y, ka > 2 ? oa.z : a.z, a.w);
   if (kb < 4) ob = make_uint4(kb > 0 ? ob.x : b.x, kb > 1 ? ob.y : b.y, kb > 2 ? ob.z : b.z, b.w);
 }
@@ -188,23 +292,46 @@ __device__ __forceinline__ const uint16_t* row_ptr(const RopeRows& r, const RowA
 }
 
 // cos and sin of a row's pairs, by its T threads. The angle in turns is reduced in fp64 to
-// [-1/2, 1/2]; what fp32 then adds is 2^-25 of a turn.
-__device__ __forceinline__ void fill_table(const RopeParams& p, const double* turns, const uint8_t* axis, const RowAt& at,
-                                           int t, float2* cs) {
-  for (int i = t; i < p.pairs; i += p.T) {
+// [-1/2, 1/2]; what fp32 then adds is 2^-25 of a turn. The position of a thread's first pair is
+// read a row ahead (`ahead`): it would come from L2 right before a barrier. Pairs that pass have
+// cos 1 and sin 0.
+struct Angles {
+  const double* turns;  // of the pairs, in shared memory
+  const uint8_t* axis;
+  int2 ahead;  // low and high half of a position
+
+  __device__ __forceinline__ int2 position(const RopeParams& p, const RowAt& at, int i) const {
     const int64_t o = at.b * p.pos_sb + at.l * p.pos_sl + axis[i];
-    const double pos = p.index64 ? (double)__ldg(static_cast<const long long*>(p.positions) + o)
-                                 : (double)__ldg(static_cast<const int*>(p.positions) + o);
-    double a = pos * turns[i];
-    a -= rint(a);
-    float s, c;
-    sincospif(2.0f * (float)a, &s, &c);
-    cs[i] = make_float2(c, s);
+    if (p.index64) return __ldg(static_cast<const int2*>(p.positions) + o);
+    return make_int2(__ldg(static_cast<const int*>(p.positions) + o), 0);
   }
-}
+  __device__ __forceinline__ void read_ahead(const RopeParams& p, const RowAt& at, int t) {
+    if (t < p.pairs) ahead = position(p, at, t);
+  }
+  __device__ __forceinline__ void fill(const RopeParams& p, const RowAt& at, int t, float* table) const {
+#pragma unroll 1
+    for (int i = t; i < p.hd / 2; i += p.T) {
+      float s = 0.0f, c = 1.0f;
+      if (i < p.pairs) {
+        const int2 v = i == t ? ahead : position(p, at, i);
+        const double pos = p.index64 ? (double)((long long)((unsigned long long)(unsigned)v.y << 32 | (unsigned)v.x)) : (double)v.x;
+        double a = pos * turns[i];
+        a -= rint(a);
+        sincospif(2.0f * (float)a, &s, &c);
+      }
+      table[i] = c, table[p.hd / 2 + i] = s * p.sign;
+    }
+  }
+};
 
 template <typename V>
 __device__ __forceinline__ V lanes_sum(V v, int lanes) {
+  if (lanes == 32) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+  }
+#pragma unroll 1
   for (int o = lanes >> 1; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
@@ -212,56 +339,229 @@ __device__ __forceinline__ V lanes_sum(V v, int lanes) {
 // fp32 sums of squares that are kept: outside, the sums are taken again in fp64.
 __device__ __forceinline__ bool in_range(float ss) { return ss >= 0x1p-80f && ss <= 0x1p+100f; }
 
-// A thread's own two vectors of a head, in shared memory: x's, then grad's where BACK. One
-// stage holds all heads of a thread; vectors of neighbouring threads are neighbours.
-template <bool BACK>
-struct Stage {
-  static constexpr int kVectors = BACK ? 4 : 2;
-  uint4* mine;  // vector 0 of head 0
-  int step;     // vectors from one to the next: the CTA's threads
-  __device__ __forceinline__ uint4* at(int k, int v) const { return mine + (k * kVectors + v) * step; }
-};
-
-template <bool FP16>
-__device__ __forceinline__ void load_weights(const RopeParams& p, const Place& q, int h, float (&wa)[8], float (&wb)[8]) {
-  load_weight8<FP16>(p.weight, p.weight_fp32, h * p.weight_sh + q.offA, wa);
-  load_weight8<FP16>(p.weight, p.weight_fp32, h * p.weight_sh + q.offB, wb);
+__device__ __forceinline__ float sum_of(uint64_t v) {
+  float a, b;
+  fused_norm_impl::upk2(v, a, b);
+  return a + b;
 }
 
-// A head's sums of x^2 and of w dn x over this thread's channels.
-template <typename Sum, bool FP16, bool HALF, bool BACK>
-__device__ __forceinline__ void unit_sums(const RopeParams& p, const Place& q, const float2* cs, const Stage<BACK>& st, int k,
-                                          Sum& xx, Sum& gx) {
-  float xa[8], xb[8];
-  widen8<FP16>(*st.at(k, 0), xa);
-  widen8<FP16>(*st.at(k, 1), xb);
-  Sum s0 = 0, s1 = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s0 += (Sum)xa[i] * (Sum)xa[i], s1 += (Sum)xb[i] * (Sum)xb[i];
-  xx += s0 + s1;
-  if (BACK) {
-    float a[8], b[8];
-    widen8<FP16>(*st.at(k, 2), a);
-    widen8<FP16>(*st.at(k, 3), b);
-    turn<HALF, -1>(p, q, cs, a, b);
-    if (p.weight) {
-      float wa[8], wb[8];
-      load_weights<FP16>(p, q, q.g + k * p.G, wa, wb);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] *= wa[i], b[i] *= wb[i];
+// The sum of eight values' squares in fp64, for the rare rows. The values are read again, and
+// the loop stays rolled: walking the registers would set the allocation of the whole kernel.
+template <bool FP16>
+__device__ __forceinline__ double exact_squares(const uint16_t* at) {
+  double s = 0.0;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const float2 e = widen16<FP16>(*(reinterpret_cast<const uint32_t*>(at) + i));
+    s = fma((double)e.y, (double)e.y, fma((double)e.x, (double)e.x, s));
+  }
+  return s;
+}
+
+// ---- forward ---------------------------------------------------------------------------------
+//
+// A row belongs to one warp (or to fewer lanes, rows sharing warps; or to the P = T / 32 warps
+// of a CTA, where there are few rows or the row is long), whose lanes hold all of it in
+// registers as it was loaded: one barrier at most, and the lane's cos and sin serve all its
+// heads. Each head's registers take the next row's vectors as soon as its output is stored, so
+// loads are in flight while the row is worked on.
+
+struct ForwardShared {
+  double turns[kMaxPairs];
+  float sums[2][kForwardThreads / 32][32];
+  double sums64[kForwardThreads / 32];
+  uint8_t axis[kMaxPairs];
+};
+static_assert(sizeof(ForwardShared) % 16 == 0, "the tables behind it are 16-byte aligned");
+inline size_t forward_shared_bytes(int rows_per_cta, int hd, int weights) {
+  return sizeof(ForwardShared) + ((size_t)2 * rows_per_cta * hd + weights) * sizeof(float);
+}
+
+template <bool FP16, int NH, int NORM, bool HALF>
+__global__ void __launch_bounds__(kForwardThreads, 1) rope_norm_rows(const __grid_constant__ RopeParams p) {
+  using namespace fused_norm_impl;
+  extern __shared__ __align__(16) unsigned char raw[];
+  ForwardShared& sh = *reinterpret_cast<ForwardShared*>(raw);
+  const int T = p.T, R = blockDim.x / T;  // R > 1 only where T <= 32
+  const int slot = threadIdx.x / T, t = threadIdx.x - slot * T;
+  const bool wide = T > 32;
+  const int lane = threadIdx.x & 31, warp = wide ? t >> 5 : 0, P = wide ? T >> 5 : 1;
+  const Place q = place_of<HALF>(p, wide ? lane : t);
+  float* const tables = reinterpret_cast<float*>(raw + sizeof(ForwardShared)) + (size_t)slot * p.hd;
+  for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) sh.turns[i] = p.turns[i], sh.axis[i] = p.axis[i];
+  float* const weights = reinterpret_cast<float*>(raw + sizeof(ForwardShared)) + (size_t)2 * R * p.hd;
+  if (NORM != BO_NORM_NONE) fill_weights<FP16, HALF>(p, weights);  // nothing without a weight
+  __syncthreads();
+
+  // Heads of a pass over the row: NH of each lane group of each warp; a norm over all heads
+  // takes one pass.
+  const int per_pass = P * NH * p.G;
+  const int head0 = warp * NH * p.G + q.g;
+  // The number of the thread's heads in the pass that starts with its head h.
+  auto heads_from = [&](int h) { return q.owns && h < p.H ? (p.H - h + p.G - 1) / p.G : 0; };
+  const int apart = q.offB - q.offA;
+  uint4 a[NH], b[NH];
+  // One head's two vectors, A at `from`; on to the thread's next head.
+  auto load = [&](const uint16_t*& from, int k, int n) {
+    if (k < n) {
+      a[k] = __ldcs(reinterpret_cast<const uint4*>(from));
+      b[k] = __ldcs(reinterpret_cast<const uint4*>(from + apart));
     }
-    s0 = s1 = 0;
+    from += p.G * p.x.sh;
+  };
+  const int n0 = heads_from(head0);
+  const uint32_t step = gridDim.x * R;
+  uint32_t row = blockIdx.x * R + slot;
+  RowAt at = row_at(p, row);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s0 += (Sum)a[i] * (Sum)xa[i], s1 += (Sum)b[i] * (Sum)xb[i];
-    gx += s0 + s1;
+  for (int k = 0; k < NH; ++k) a[k] = b[k] = make_uint4(0, 0, 0, 0);
+  Angles angles{sh.turns, sh.axis, make_int2(0, 0)};
+  if (row < p.rows) {
+    angles.read_ahead(p, at, t);
+    const uint16_t* from = row_ptr(p.x, at) + (head0 * p.x.sh + q.offA);
+#pragma unroll
+    for (int k = 0; k < NH; ++k) load(from, k, n0);
+  }
+  // the lanes of a warp go round together; step + rows < 2^32, the host bounds both
+  for (int parity = 0; wide ? row < p.rows : __any_sync(0xFFFFFFFFu, row < p.rows); row += step, parity ^= 1) {
+    const bool live = row < p.rows;
+    const RowAt next = row_at(p, row + step);
+    const bool more = live && row + step < p.rows;
+    float* const table = tables + (size_t)parity * R * p.hd;
+    if (live) angles.fill(p, at, t, table);
+    if (more) angles.read_ahead(p, next, t);
+    const uint16_t* const xr = row_ptr(p.x, at);
+    float rho = 1.0f;
+    float part = 0.0f;  // of the row's squares: pairs of heads, then the pairs in order, whatever NH is
+    if (NORM == BO_NORM_ALL) {
+#pragma unroll
+      for (int k = 0; k < NH; k += 2) {
+        uint64_t s[2] = {0, 0};
+#pragma unroll
+        for (int i = k; i < k + 2 && i < NH; ++i) {
+          uint64_t x[4], y[4];
+          split<FP16, HALF>(a[i], b[i], x, y);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[0] = fma2(x[j], x[j], s[0]), s[1] = fma2(y[j], y[j], s[1]);
+        }
+        part += sum_of(add2(s[0], s[1]));
+      }
+      if (wide) sh.sums[parity][warp][lane] = part;
+    }
+    if (wide) __syncthreads();
+    else __syncwarp();
+    const Turn turns = load_turn(p, q, table);
+    if (NORM == BO_NORM_ALL) {
+      if (wide) {
+        part = sh.sums[parity][0][lane];
+        for (int w = 1; w < P; ++w) part += sh.sums[parity][w][lane];
+      }
+      const float ss = lanes_sum(part, wide ? 32 : T);
+      rho = rsqrtf(fmaf(ss, p.inv_n, p.eps));
+      const bool odd = live && !in_range(ss);
+      if (__any_sync(0xFFFFFFFFu, odd)) {  // a wide row's threads agree
+        double e = 0.0;
+#pragma unroll 1
+        for (int k = 0; k < NH; ++k)
+          if (live && k < n0) {
+            const uint16_t* v = xr + (head0 + k * p.G) * p.x.sh;
+            e += exact_squares<FP16>(v + q.offA) + exact_squares<FP16>(v + q.offB);
+          }
+        e = lanes_sum(e, wide ? 32 : T);
+        if (wide) {
+          if (lane == 0) sh.sums64[warp] = e;
+          __syncthreads();
+          e = 0.0;
+          for (int w = 0; w < P; ++w) e += sh.sums64[w];
+          __syncthreads();
+        }
+        if (odd) rho = (float)rsqrt(e * p.inv_n64 + p.eps64);
+      }
+    }
+    uint16_t* const out = const_cast<uint16_t*>(row_ptr(p.out, at));
+    for (int base = 0; base < (NORM == BO_NORM_ALL ? 1 : p.H); base += per_pass) {
+      const bool last = NORM == BO_NORM_ALL || base + per_pass >= p.H;
+      const int first = here(base + head0);
+      uint16_t* to = out + (first * p.out.sh + q.offA);
+      const uint16_t* from = (last ? row_ptr(p.x, next) + head0 * p.x.sh : xr + (first + per_pass) * p.x.sh) + q.offA;
+      int unit = first * p.weight_sh + q.u;
+      const int n = live ? NORM == BO_NORM_ALL ? n0 : heads_from(first) : 0;
+      const int n_next = last ? (more ? n0 : 0) : live ? heads_from(first + per_pass) : 0;
+#pragma unroll
+      for (int k = 0; k < NH; ++k) {
+        const bool mine = k < n;
+        uint64_t x[4], y[4];
+        if (NORM == BO_NORM_HEAD) {
+          split<FP16, HALF>(a[k], b[k], x, y);
+          uint64_t s[2] = {0, 0};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[0] = fma2(x[j], x[j], s[0]), s[1] = fma2(y[j], y[j], s[1]);
+          const float ss = lanes_sum(q.owns ? sum_of(add2(s[0], s[1])) : 0.0f, p.W);
+          rho = rsqrtf(fmaf(ss, p.inv_n, p.eps));
+          const bool odd = mine && !in_range(ss);
+          if (__any_sync(0xFFFFFFFFu, odd)) {
+            double e = 0.0;
+            const uint16_t* v = xr + (first + k * p.G) * p.x.sh;
+            if (mine) e = exact_squares<FP16>(v + q.offA) + exact_squares<FP16>(v + q.offB);
+            e = lanes_sum(e, p.W);
+            if (odd) rho = (float)rsqrt(e * p.inv_n64 + p.eps64);
+          }
+        }
+        if (mine) {
+          split<FP16, HALF>(here(a[k]), here(b[k]), x, y);
+          if (NORM != BO_NORM_NONE) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = mul2(x[j], pk2(rho, rho)), y[j] = mul2(y[j], pk2(rho, rho));
+            if (p.weight) weigh(weights + weight_at(unit), x, y);
+          }
+          turn<HALF, 1>(p, q, turns, x, y);
+          uint4 oa, ob;
+          join<FP16, HALF>(x, y, oa, ob);
+          if (NORM == BO_NORM_NONE && p.passes) keep_passing<HALF>(p, q, a[k], b[k], oa, ob);  // a NaN keeps its bits too
+          __stcs(reinterpret_cast<uint4*>(to), oa);
+          __stcs(reinterpret_cast<uint4*>(to + apart), ob);
+        }
+        to += p.G * p.out.sh, unit += p.G * p.weight_sh;
+        load(from, k, n_next);
+      }
+    }
+    at = next;
   }
 }
 
-// The same in fp64, for the rare rows; out of line.
-template <bool FP16, bool HALF, bool BACK>
-__device__ __noinline__ double2 exact_sums(const RopeParams& p, const Place& q, const float2* cs, const Stage<BACK>& st, int k) {
+// ---- gradient --------------------------------------------------------------------------------
+//
+// One row per CTA turn (rows of 32 lanes or fewer share warps) with NH heads to a thread, since
+// a thread also keeps dn between the sums and the output, and the sums of dweight over its rows.
+// Each thread copies its own vectors of the next two rows to shared memory while it works on the
+// present one, so no registers wait for loads and nobody else has to be waited for.
+
+// A thread's own two vectors of a head, in shared memory: x's, then grad's. One stage holds all
+// heads of a thread; vectors of neighbouring threads are neighbours.
+struct Stage {
+  uint4* mine;  // vector 0 of head 0
+  int step;     // vectors from one to the next: the CTA's threads
+  __device__ __forceinline__ uint4* at(int k, int v) const { return mine + (k * 4 + v) * step; }
+};
+
+// A head's sums of x^2 and of w dn x over this thread's channels in fp64, for the rare rows.
+template <bool FP16, bool HALF>
+__device__ __noinline__ double2 exact_sums(const RopeParams& p, const Place& q, const float* table, const Stage& st, int k, const float* weight) {
+  uint64_t x[2][4], d[2][4];
+  split<FP16, HALF>(*st.at(k, 0), *st.at(k, 1), x[0], x[1]);
+  split<FP16, HALF>(*st.at(k, 2), *st.at(k, 3), d[0], d[1]);
+  turn<HALF, -1>(p, q, load_turn(p, q, table), d[0], d[1]);
   double2 r = make_double2(0.0, 0.0);
-  unit_sums<double, FP16, HALF, BACK>(p, q, cs, st, k, r.x, r.y);
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 4; ++j) {
+      float xe[2], de[2];
+      fused_norm_impl::upk2(x[i][j], xe[0], xe[1]);
+      fused_norm_impl::upk2(d[i][j], de[0], de[1]);
+      for (int e = 0; e < 2; ++e) {
+        r.x = fma((double)xe[e], (double)xe[e], r.x);
+        r.y = fma((p.weight ? (double)weight[64 * i + j / 2 * 32 + j % 2 * 2 + e] : 1.0) * (double)de[e], (double)xe[e], r.y);
+      }
+    }
   return r;
 }
 
@@ -269,180 +569,181 @@ __device__ __forceinline__ void copy_async(uint4* to, const uint16_t* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
 }
 
-// Shared memory of a CTA: the frequency table, sums; then three tables of (cos, sin) per row
-// slot; then three stages of rows. A row's table is written before the barrier of the row
+// Shared memory of a CTA: the frequency table, sums; then three tables of cos and sin per row
+// slot, the weights, and the stages of rows (three, or as many as fit). A row's table is written before the barrier of the row
 // ahead of it and read up to the barrier of the row behind it, so its buffer comes round again
 // at the third row.
 constexpr int kStages = 3;
-struct RopeShared {
+struct BackwardShared {
   double turns[kMaxPairs];
   double sums64[2][kRopeThreads / 32];
   float2 sums[kStages][kRopeThreads / 32];
   uint8_t axis[kMaxPairs];
 };
-__host__ __device__ inline size_t rope_tables_bytes(int rows_per_cta, int pairs) {
-  return ((size_t)kStages * rows_per_cta * pairs * sizeof(float2) + 15) / 16 * 16;
+__host__ __device__ inline size_t backward_tables_bytes(int rows_per_cta, int hd) {
+  return (size_t)kStages * rows_per_cta * hd * sizeof(float);
 }
-inline size_t rope_shared_bytes(int rows_per_cta, int pairs, int threads, int nh, bool back) {
-  const size_t rows = (size_t)kStages * threads * nh * (back ? 4 : 2) * 16;
-  return sizeof(RopeShared) + rope_tables_bytes(rows_per_cta, pairs) + rows;
+inline size_t backward_shared_bytes(int rows_per_cta, int hd, int weights, int threads, int nh, int stages) {
+  return sizeof(BackwardShared) + backward_tables_bytes(rows_per_cta, hd) + (size_t)weights * sizeof(float) + (size_t)stages * threads * nh * 4 * 16;
 }
-static_assert(sizeof(RopeShared) % 16 == 0, "what follows is 16-byte aligned");
+static_assert(sizeof(BackwardShared) % 16 == 0, "what follows is 16-byte aligned");
 
-// BACK: the gradient. DW: it sums dweight's partials too (needs a norm).
-template <bool FP16, int NH, int NORM, bool HALF, bool BACK, bool DW>
-__global__ void __launch_bounds__(kRopeThreads, 1) rope_norm_rows(const __grid_constant__ RopeParams p) {
+// NORM: over the head or over all. DW: the kernel sums dweight's partials too.
+template <bool FP16, int NH, int NORM, bool HALF, bool DW>
+__global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) rope_norm_gradient(const __grid_constant__ RopeParams p) {
+  using namespace fused_norm_impl;
   extern __shared__ __align__(16) unsigned char raw[];
-  RopeShared& sh = *reinterpret_cast<RopeShared*>(raw);
-  float2* const tables = reinterpret_cast<float2*>(raw + sizeof(RopeShared));
-  constexpr bool READ_X = !BACK || NORM != BO_NORM_NONE;
+  BackwardShared& sh = *reinterpret_cast<BackwardShared*>(raw);
+  float* const tables = reinterpret_cast<float*>(raw + sizeof(BackwardShared));
   const int T = p.T, R = blockDim.x / T;  // R > 1 only where T <= 32
   const int slot = threadIdx.x / T, t = threadIdx.x - slot * T;
   const bool wide = T > 32;
   const Place q = place_of<HALF>(p, t);
-  uint4* const stages = reinterpret_cast<uint4*>(raw + sizeof(RopeShared) + rope_tables_bytes(R, p.pairs)) + threadIdx.x;
+  float* const weights = tables + (size_t)kStages * R * p.hd;
+  uint4* const stages = reinterpret_cast<uint4*>(weights + weight_floats(p.weight_units)) + threadIdx.x;
   for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) sh.turns[i] = p.turns[i], sh.axis[i] = p.axis[i];
+  fill_weights<FP16, HALF>(p, weights);
   __syncthreads();
-  auto table = [&](int buf) { return tables + (size_t)(buf * R + slot) * p.pairs; };
-  auto stage = [&](int buf) {
-    return Stage<BACK>{stages + (size_t)buf * NH * Stage<BACK>::kVectors * blockDim.x, (int)blockDim.x};
-  };
+  auto weight = [&](int k) { return weights + weight_at((q.g + k * p.G) * p.weight_sh + q.u); };
+  auto table = [&](int buf) { return tables + (size_t)(buf * R + slot) * p.hd; };
+  auto stage = [&](int buf) { return Stage{stages + (size_t)buf * NH * 4 * blockDim.x, (int)blockDim.x}; };
   auto has = [&](int k) { return q.owns && q.g + k * p.G < p.H; };
-  auto fetch = [&](uint32_t row, int buf) {
-    if (row < p.rows) {
-      const RowAt at = row_at(p, row);
-      const Stage<BACK> st = stage(buf);
+  auto fetch = [&](const RowAt& at, bool live, int buf) {
+    if (live) {
+      const Stage st = stage(buf);
+      const uint16_t *x = row_ptr(p.x, at) + q.g * p.x.sh, *d = row_ptr(p.dy, at) + q.g * p.dy.sh;
 #pragma unroll
-      for (int k = 0; k < NH; ++k) {
+      for (int k = 0; k < NH; ++k, x += p.G * p.x.sh, d += p.G * p.dy.sh) {
         if (!has(k)) continue;
-        const int h = q.g + k * p.G;
-        if (READ_X) {
-          const uint16_t* b = row_ptr(p.x, at) + h * p.x.sh;
-          copy_async(st.at(k, 0), b + q.offA);
-          copy_async(st.at(k, 1), b + q.offB);
-        }
-        if (BACK) {
-          const uint16_t* b = row_ptr(p.dy, at) + h * p.dy.sh;
-          copy_async(st.at(k, 2), b + q.offA);
-          copy_async(st.at(k, 3), b + q.offB);
-        }
+        copy_async(st.at(k, 0), x + q.offA);
+        copy_async(st.at(k, 1), x + q.offB);
+        copy_async(st.at(k, 2), d + q.offA);
+        copy_async(st.at(k, 3), d + q.offB);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   constexpr int NACC = NORM == BO_NORM_ALL ? NH : 1;
-  float acc[DW ? NACC : 1][16];
+  uint64_t acc[DW ? NACC : 1][8];
 #pragma unroll
   for (int k = 0; k < (DW ? NACC : 1); ++k)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[k][i] = 0.0f;
+    for (int i = 0; i < 8; ++i) acc[k][i] = 0;
 
-  // The output of one head, and its part of dweight; m = mean(w dn x) rho.
-  auto finish = [&](const float2* cs, const Stage<BACK>& st, uint16_t* ob, int k, float rho, float m) {
+  uint64_t dx[NH][4], dy[NH][4];  // dn of the present row
+  // dn of head k, and its sums of x^2 and w dn x.
+  auto begin = [&](const Turn& turns, const Stage& st, int k) {
+    uint64_t x[4], y[4], sx[2] = {0, 0}, sg[2] = {0, 0};
+    split<FP16, HALF>(*st.at(k, 2), *st.at(k, 3), dx[k], dy[k]);
+    turn<HALF, -1>(p, q, turns, dx[k], dy[k]);
+    split<FP16, HALF>(*st.at(k, 0), *st.at(k, 1), x, y);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sx[0] = fma2(x[j], x[j], sx[0]), sx[1] = fma2(y[j], y[j], sx[1]);
+    uint64_t gx[4], gy[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) gx[j] = dx[k][j], gy[j] = dy[k][j];
+    if (p.weight) weigh(weight(k), gx, gy);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sg[0] = fma2(gx[j], x[j], sg[0]), sg[1] = fma2(gy[j], y[j], sg[1]);
+    return make_float2(sum_of(add2(sx[0], sx[1])), sum_of(add2(sg[0], sg[1])));
+  };
+  // The output of head k, and its part of dweight; m = mean(w dn x) rho.
+  auto finish = [&](const Stage& st, uint16_t* ob, int k, float rho, float m) {
     const int h = q.g + k * p.G;
-    float a[8], b[8];
-    widen8<FP16>(*st.at(k, BACK ? 2 : 0), a);
-    widen8<FP16>(*st.at(k, BACK ? 3 : 1), b);
-    if (!BACK) {
-      if (NORM != BO_NORM_NONE) {
+    const uint64_t rr = pk2(rho, rho), mm = pk2(-m, -m);
+    uint64_t x[4], y[4];
+    split<FP16, HALF>(*st.at(k, 0), *st.at(k, 1), x, y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] *= rho, b[i] *= rho;
-        if (p.weight) {
-          float wa[8], wb[8];
-          load_weights<FP16>(p, q, h, wa, wb);
+    for (int j = 0; j < 4; ++j) x[j] = mul2(x[j], rr), y[j] = mul2(y[j], rr);
+    if (DW) {
+      uint64_t(&s)[8] = acc[NORM == BO_NORM_ALL ? k : 0];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] *= wa[i], b[i] *= wb[i];
-        }
-      }
-      turn<HALF, 1>(p, q, cs, a, b);
-    } else {
-      turn<HALF, -1>(p, q, cs, a, b);  // dn, the same values as in the sums
-      if (NORM != BO_NORM_NONE) {
-        float na[8], nb[8];
-        widen8<FP16>(*st.at(k, 0), na);
-        widen8<FP16>(*st.at(k, 1), nb);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) na[i] *= rho, nb[i] *= rho;
-        if (DW) {
-          float(&s)[16] = acc[NORM == BO_NORM_ALL ? k : 0];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[i] = fmaf(a[i], na[i], s[i]), s[8 + i] = fmaf(b[i], nb[i], s[8 + i]);
-        }
-        if (p.weight) {
-          float wa[8], wb[8];
-          load_weights<FP16>(p, q, h, wa, wb);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] *= wa[i], b[i] *= wb[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = rho * fmaf(-na[i], m, a[i]), b[i] = rho * fmaf(-nb[i], m, b[i]);
-      }
+      for (int j = 0; j < 4; ++j) s[j] = fma2(dx[k][j], x[j], s[j]), s[4 + j] = fma2(dy[k][j], y[j], s[4 + j]);
     }
-    uint4 va = pack8<FP16>(a), vb = pack8<FP16>(b);
-    if (NORM == BO_NORM_NONE) {  // channels that pass keep their bits, a NaN's too
-      keep_passing<HALF>(p, q, *st.at(k, BACK ? 2 : 0), *st.at(k, BACK ? 3 : 1), va, vb);
-    }
-    __stcs(reinterpret_cast<uint4*>(ob + (h * p.out.sh + q.offA)), va);
-    __stcs(reinterpret_cast<uint4*>(ob + (h * p.out.sh + q.offB)), vb);
+    if (p.weight) weigh(weight(k), dx[k], dy[k]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = mul2(rr, fma2(x[j], mm, dx[k][j])), y[j] = mul2(rr, fma2(y[j], mm, dy[k][j]));
+    uint4 va, vb;
+    join<FP16, HALF>(x, y, va, vb);
+    uint16_t* const to = ob + here(h) * p.out.sh;
+    __stcs(reinterpret_cast<uint4*>(to + q.offA), va);
+    __stcs(reinterpret_cast<uint4*>(to + q.offB), vb);
   };
   // Sums that fp32 does not hold.
-  auto outside = [](float xx, float gx) { return !(in_range(xx) && (!BACK || fabsf(gx) <= 0x1p+100f)); };
+  auto outside = [](float xx, float gx) { return !(in_range(xx) && fabsf(gx) <= 0x1p+100f); };
 
   const uint32_t step = gridDim.x * R;
   uint32_t base = blockIdx.x * R;
-  fetch(base + slot, 0);
-  fetch(base + slot + step, 1);  // rows + 2 step < 2^32: the host bounds both
-  if (base + slot < p.rows) fill_table(p, sh.turns, sh.axis, row_at(p, base + slot), t, table(0));
+  RowAt at = row_at(p, base + slot), at1 = row_at(p, base + slot + step);
+  if (p.stages > 1) fetch(at, base + slot < p.rows, 0);
+  if (p.stages > 2) fetch(at1, base + slot + step < p.rows, 1);  // rows + 2 step < 2^32: the host bounds both
+  Angles angles{sh.turns, sh.axis, make_int2(0, 0)};
+  if (base + slot < p.rows) {
+    angles.read_ahead(p, at, t);
+    angles.fill(p, at, t, table(0));
+  }
+  if (base + slot + step < p.rows) angles.read_ahead(p, at1, t);
   if (wide) __syncthreads();
   else __syncwarp();
 
-  for (int buf = 0, ahead = 1; base < p.rows; base += step, buf = ahead, ahead = ahead == kStages - 1 ? 0 : ahead + 1) {
-    const uint32_t row = base + slot, next = row + step;
-    const RowAt at = row_at(p, row);
+  for (int buf = 0, ahead = 1, now = 0; base < p.rows; base += step, buf = ahead, ahead = ahead == kStages - 1 ? 0 : ahead + 1,
+           now = now == p.stages - 1 ? 0 : now + 1) {
+    const uint32_t row = base + slot;
     const bool live = row < p.rows;
-    const float2* const cs = table(buf);
-    const Stage<BACK> st = stage(buf);
-    fetch(next + step, ahead == kStages - 1 ? 0 : ahead + 1);
-    asm volatile("cp.async.wait_group 2;" ::: "memory");  // this row's vectors are here
+    const Stage st = stage(now);
+    const RowAt at2 = row_at(p, row + 2 * step);
+    const Turn turns = load_turn(p, q, table(buf));
+    // the stage before this one is free; then this row's vectors are here
+    if (p.stages == 3) {
+      fetch(at2, row + 2 * step < p.rows, now == 0 ? 2 : now - 1);
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+    } else if (p.stages == 2) {
+      fetch(at1, row + step < p.rows, now ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      fetch(at, live, 0);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
 
     float2 all = make_float2(0.0f, 0.0f);
     if (NORM == BO_NORM_ALL) {
 #pragma unroll
       for (int k = 0; k < NH; ++k)
-        if (live && has(k)) unit_sums<float, FP16, HALF, BACK>(p, q, cs, st, k, all.x, all.y);
+        if (live && has(k)) {
+          const float2 s = begin(turns, st, k);
+          all.x += s.x, all.y += s.y;
+        }
       all.x = lanes_sum(all.x, wide ? 32 : T);
-      if (BACK) all.y = lanes_sum(all.y, wide ? 32 : T);
+      all.y = lanes_sum(all.y, wide ? 32 : T);
       if (wide && (t & 31) == 0) sh.sums[buf][t >> 5] = all;
     }
-    if (next < p.rows) fill_table(p, sh.turns, sh.axis, row_at(p, next), t, table(ahead));
+    if (row + step < p.rows) angles.fill(p, at1, t, table(ahead));
+    if (row + 2 * step < p.rows) angles.read_ahead(p, at2, t);
     if (wide) __syncthreads();
     else __syncwarp();
 
     uint16_t* const ob = const_cast<uint16_t*>(row_ptr(p.out, at));
-    if (NORM == BO_NORM_NONE) {
-#pragma unroll
-      for (int k = 0; k < NH; ++k)
-        if (live && has(k)) finish(cs, st, ob, k, 1.0f, 0.0f);
-    } else if (NORM == BO_NORM_HEAD) {
+    if (NORM == BO_NORM_HEAD) {
 #pragma unroll
       for (int k = 0; k < NH; ++k) {
         float2 s = make_float2(0.0f, 0.0f);
         const bool mine = live && has(k);
-        if (mine) unit_sums<float, FP16, HALF, BACK>(p, q, cs, st, k, s.x, s.y);
+        if (mine) s = begin(turns, st, k);
         s.x = lanes_sum(s.x, p.W);
-        if (BACK) s.y = lanes_sum(s.y, p.W);
+        s.y = lanes_sum(s.y, p.W);
         float rho = rsqrtf(fmaf(s.x, p.inv_n, p.eps)), m = s.y * p.inv_n * rho;
         if (__any_sync(0xFFFFFFFFu, mine && outside(s.x, s.y))) {
-          double2 e = mine ? exact_sums<FP16, HALF, BACK>(p, q, cs, st, k) : make_double2(0.0, 0.0);
+          double2 e = make_double2(0.0, 0.0);
+          if (mine) e = exact_sums<FP16, HALF>(p, q, table(buf), st, k, weight(k));
           e.x = lanes_sum(e.x, p.W);
-          if (BACK) e.y = lanes_sum(e.y, p.W);
+          e.y = lanes_sum(e.y, p.W);
           if (outside(s.x, s.y)) {
             const double f = rsqrt(e.x * p.inv_n64 + p.eps64);
             rho = (float)f, m = (float)(e.y * p.inv_n64 * f);
           }
         }
-        if (mine) finish(cs, st, ob, k, rho, m);
+        if (mine) finish(st, ob, k, rho, m);
       }
     } else {
       if (wide) {
@@ -456,13 +757,14 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_norm_rows(const __grid_c
       const bool odd = live && outside(all.x, all.y);
       if (wide ? odd : (bool)__any_sync(0xFFFFFFFFu, odd)) {  // the same for all threads that meet below
         double2 e = make_double2(0.0, 0.0);
+#pragma unroll 1
         for (int k = 0; k < NH; ++k)
           if (live && has(k)) {
-            const double2 one = exact_sums<FP16, HALF, BACK>(p, q, cs, st, k);
+            const double2 one = exact_sums<FP16, HALF>(p, q, table(buf), st, k, weight(k));
             e.x += one.x, e.y += one.y;
           }
         e.x = lanes_sum(e.x, wide ? 32 : T);
-        if (BACK) e.y = lanes_sum(e.y, wide ? 32 : T);
+        e.y = lanes_sum(e.y, wide ? 32 : T);
         if (wide) {
           if ((t & 31) == 0) sh.sums64[0][t >> 5] = e.x, sh.sums64[1][t >> 5] = e.y;
           __syncthreads();
@@ -477,20 +779,27 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_norm_rows(const __grid_c
       }
 #pragma unroll
       for (int k = 0; k < NH; ++k)
-        if (live && has(k)) finish(cs, st, ob, k, rho, m);
+        if (live && has(k)) finish(st, ob, k, rho, m);
     }
+    at = at1, at1 = at2;
   }
 
   if (!DW) return;
   // ---- this CTA's part of dweight --------------------------------------------------------------
   float* const part = p.partial + (size_t)blockIdx.x * (NORM == BO_NORM_ALL ? p.H * p.hd : p.hd);
+  // value i of a thread: side i / 8, element (i / 2) % 4, half i % 2
+  auto value = [&](int k, int i) {
+    float v[2];
+    upk2(acc[k][i / 2], v[0], v[1]);
+    return v[i & 1];
+  };
   if (NORM == BO_NORM_ALL && wide) {  // every channel of the token has one thread
 #pragma unroll
     for (int k = 0; k < NACC; ++k) {
       if (!has(k)) continue;
       float* o = part + (q.g + k * p.G) * p.hd;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[q.offA + i] = acc[k][i], o[q.offB + i] = acc[k][8 + i];
+      for (int i = 0; i < 16; ++i) o[channel_of<HALF>(q, (i / 2) % 4, i & 1, i / 8)] = value(k, i);
     }
     return;
   }
@@ -498,9 +807,12 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_norm_rows(const __grid_c
   // through the first stage (every thread is past its rows, and its copies have landed).
   asm volatile("cp.async.wait_all;" ::: "memory");
   const int span = NORM == BO_NORM_ALL ? T : p.W;
+  float v[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    for (int o = span; o < 32; o <<= 1) acc[0][i] += __shfl_xor_sync(0xFFFFFFFFu, acc[0][i], o);
+  for (int i = 0; i < 16; ++i) {
+    v[i] = value(0, i);
+    for (int o = span; o < 32; o <<= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+  }
   float* const sums = reinterpret_cast<float*>(stages - threadIdx.x);  // 16 values of `span` lanes
   for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
     __syncthreads();
@@ -508,7 +820,7 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_norm_rows(const __grid_c
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float& s = sums[i * 32 + (threadIdx.x & 31)];
-        s = (w ? s : 0.0f) + acc[0][i];
+        s = (w ? s : 0.0f) + v[i];
       }
     }
   }
@@ -516,41 +828,52 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_norm_rows(const __grid_c
   if ((int)threadIdx.x < span && has(0)) {
     float* o = part + (NORM == BO_NORM_ALL ? q.g * p.hd : 0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[q.offA + i] = sums[i * 32 + threadIdx.x], o[q.offB + i] = sums[(8 + i) * 32 + threadIdx.x];
+    for (int i = 0; i < 16; ++i) o[channel_of<HALF>(q, (i / 2) % 4, i & 1, i / 8)] = sums[i * 32 + threadIdx.x];
   }
 }
 
 using RopeKernel = void (*)(RopeParams);
 
-// One kernel for (threads' heads, norm, pairing, gradient, dweight); the two element types are
-// compiled in files of their own.
+// Kernels for (threads' heads, norm, pairing); the two element types are compiled in files of
+// their own. Forward: 1, 2 or 4 heads, and 6 or 10 for a norm over all; gradient: 1, 2 or 4.
 template <bool FP16>
-RopeKernel pick_rope(int nh, int norm, bool half, bool back, bool dw);
-extern template RopeKernel pick_rope<false>(int, int, bool, bool, bool);
-extern template RopeKernel pick_rope<true>(int, int, bool, bool, bool);
+RopeKernel pick_rope(int nh, int norm, bool half);
+template <bool FP16>
+RopeKernel pick_rope_gradient(int nh, int norm, bool half, bool dw);
+extern template RopeKernel pick_rope<false>(int, int, bool);
+extern template RopeKernel pick_rope<true>(int, int, bool);
+extern template RopeKernel pick_rope_gradient<false>(int, int, bool, bool);
+extern template RopeKernel pick_rope_gradient<true>(int, int, bool, bool);
 
-template <bool FP16, int NH, int NORM, bool HALF>
-RopeKernel pick_rope_pass(bool back, bool dw) {
-  if (!back) return rope_norm_rows<FP16, NH, NORM, HALF, false, false>;
-  if (NORM != BO_NORM_NONE && dw) return rope_norm_rows<FP16, NH, NORM, HALF, true, NORM != BO_NORM_NONE>;
-  return rope_norm_rows<FP16, NH, NORM, HALF, true, false>;
-}
-template <bool FP16, int NH>
-RopeKernel pick_rope_norm(int norm, bool half, bool back, bool dw) {
-  switch (norm) {
-    case BO_NORM_NONE:
-      return half ? pick_rope_pass<FP16, NH, BO_NORM_NONE, true>(back, dw) : pick_rope_pass<FP16, NH, BO_NORM_NONE, false>(back, dw);
-    case BO_NORM_HEAD:
-      return half ? pick_rope_pass<FP16, NH, BO_NORM_HEAD, true>(back, dw) : pick_rope_pass<FP16, NH, BO_NORM_HEAD, false>(back, dw);
-    default:
-      return half ? pick_rope_pass<FP16, NH, BO_NORM_ALL, true>(back, dw) : pick_rope_pass<FP16, NH, BO_NORM_ALL, false>(back, dw);
+template <bool FP16, int NORM, bool HALF>
+RopeKernel pick_rope_heads(int nh) {
+  if constexpr (NORM == BO_NORM_ALL) {
+    if (nh == 6) return rope_norm_rows<FP16, 6, NORM, HALF>;
+    if (nh == 10) return rope_norm_rows<FP16, 10, NORM, HALF>;
   }
+  return nh == 1 ? rope_norm_rows<FP16, 1, NORM, HALF> : nh == 2 ? rope_norm_rows<FP16, 2, NORM, HALF> : rope_norm_rows<FP16, 4, NORM, HALF>;
+}
+template <bool FP16, int NORM, bool HALF, bool DW>
+RopeKernel pick_rope_gradient_heads(int nh) {
+  return nh == 1   ? rope_norm_gradient<FP16, 1, NORM, HALF, DW>
+         : nh == 2 ? rope_norm_gradient<FP16, 2, NORM, HALF, DW>
+                   : rope_norm_gradient<FP16, 4, NORM, HALF, DW>;
 }
 template <bool FP16>
-RopeKernel pick_rope(int nh, int norm, bool half, bool back, bool dw) {
-  return nh == 1   ? pick_rope_norm<FP16, 1>(norm, half, back, dw)
-         : nh == 2 ? pick_rope_norm<FP16, 2>(norm, half, back, dw)
-                   : pick_rope_norm<FP16, 4>(norm, half, back, dw);
+RopeKernel pick_rope(int nh, int norm, bool half) {
+  if (norm == BO_NORM_NONE) return half ? pick_rope_heads<FP16, BO_NORM_NONE, true>(nh) : pick_rope_heads<FP16, BO_NORM_NONE, false>(nh);
+  if (norm == BO_NORM_HEAD) return half ? pick_rope_heads<FP16, BO_NORM_HEAD, true>(nh) : pick_rope_heads<FP16, BO_NORM_HEAD, false>(nh);
+  return half ? pick_rope_heads<FP16, BO_NORM_ALL, true>(nh) : pick_rope_heads<FP16, BO_NORM_ALL, false>(nh);
+}
+template <bool FP16, int NORM>
+RopeKernel pick_rope_gradient_norm(int nh, bool half, bool dw) {
+  if (half) return dw ? pick_rope_gradient_heads<FP16, NORM, true, true>(nh) : pick_rope_gradient_heads<FP16, NORM, true, false>(nh);
+  return dw ? pick_rope_gradient_heads<FP16, NORM, false, true>(nh) : pick_rope_gradient_heads<FP16, NORM, false, false>(nh);
+}
+template <bool FP16>
+RopeKernel pick_rope_gradient(int nh, int norm, bool half, bool dw) {
+  return norm == BO_NORM_HEAD ? pick_rope_gradient_norm<FP16, BO_NORM_HEAD>(nh, half, dw)
+                              : pick_rope_gradient_norm<FP16, BO_NORM_ALL>(nh, half, dw);
 }
 
 }  // namespace block_ops
