@@ -1,0 +1,5 @@
+#include "rope_norm_kernel.cuh"
+
+namespace block_ops {
+template RopeKernel pick_rope_gradient<false>(int, int, bool, bool, bool);
+}

@@ -319,16 +319,17 @@ fn_status rope_norm_create(rope_norm_t* out, const rn_config* cfg) {
   rope_norm_s* h = new (std::nothrow) rope_norm_s;
   if (!h) return FN_ERR_INVALID_ARG;
   h->cfg = c;
-  const int units = c.has_weight ? weight_values(c) / 16 : 0, weights = weight_floats(units);
+  const bool pass = 2 * pairs < c.head_dim;
+  const int units = c.norm != BO_NORM_NONE ? weight_values(c) / 16 : 0, weights = weight_floats(units);
   for (int i : {kForward, kFew, kGradient}) {
     RopeShape& s = h->shape[i];
     s = i == kGradient ? backward_shape(c.heads, c.head_dim) : forward_shape(c.heads, c.head_dim, c.norm, i == kFew);
     if (i != kGradient) {
-      s.kernel = c.dtype == BO_FP16 ? pick_rope<true>(s.nh, c.norm, c.half_pairs) : pick_rope<false>(s.nh, c.norm, c.half_pairs);
+      s.kernel = c.dtype == BO_FP16 ? pick_rope<true>(s.nh, c.norm, c.half_pairs, pass) : pick_rope<false>(s.nh, c.norm, c.half_pairs, pass);
       s.smem = forward_shared_bytes(s.rows_per_cta, c.head_dim, weights);
     } else if (c.norm != BO_NORM_NONE) {
-      s.kernel = c.dtype == BO_FP16 ? pick_rope_gradient<true>(s.nh, c.norm, c.half_pairs, sums_dweight(c))
-                                    : pick_rope_gradient<false>(s.nh, c.norm, c.half_pairs, sums_dweight(c));
+      s.kernel = c.dtype == BO_FP16 ? pick_rope_gradient<true>(s.nh, c.norm, c.half_pairs, sums_dweight(c), pass)
+                                    : pick_rope_gradient<false>(s.nh, c.norm, c.half_pairs, sums_dweight(c), pass);
       for (s.stages = kStages; s.stages >= 1; --s.stages) {
         s.smem = backward_shared_bytes(s.rows_per_cta, c.head_dim, weights, s.T * s.rows_per_cta, s.nh, s.stages);
         if (s.smem <= kMaxShared) break;
@@ -338,7 +339,6 @@ fn_status rope_norm_create(rope_norm_t* out, const rn_config* cfg) {
   RopeParams& p = h->base;
   std::memset(&p, 0, sizeof(p));
   p.H = c.heads, p.hd = c.head_dim, p.units = c.head_dim / 16, p.pairs = (int)pairs;
-  p.passes = 2 * pairs < c.head_dim;
   p.sign = 1.0f;
   p.index64 = c.index64, p.weight_fp32 = c.weight_fp32;
   p.weight_sh = c.norm == BO_NORM_ALL ? c.head_dim / 16 : 0;

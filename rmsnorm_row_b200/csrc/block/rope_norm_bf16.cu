@@ -1,6 +1,5 @@
 #include "rope_norm_kernel.cuh"
 
 namespace block_ops {
-template RopeKernel pick_rope<false>(int, int, bool);
-template RopeKernel pick_rope_gradient<false>(int, int, bool, bool);
+template RopeKernel pick_rope<false>(int, int, bool, bool);
 }

@@ -55,7 +55,6 @@ struct RopeParams {
   DivU32 div_L;
   int H, hd, units, pairs;  // units of a head (hd / 16), pairs that turn
   int W, T, G;              // lanes of a head, threads of a row, lane groups (of a warp, in the forward kernel)
-  int passes;               // some pairs of a head do not turn
   int stages;               // rows of the gradient kernel in shared memory: 1 to 3
   float sign;               // -1 turns the other way
   int index64, weight_fp32;
@@ -181,7 +180,7 @@ __device__ __forceinline__ int channel_of(const Place& q, int j, int half, int s
 
 // The weights in shared memory as fp32 in the order of split units, which CTAs keep for all
 // their rows (widening and addressing them in global memory took a fifth of a row's
-// instructions). The four quarters of eight units' values alternate, so that eight lanes read
+// instructions), ones without a weight. The four quarters of eight units' values alternate, so that eight lanes read
 // 128 bytes without bank conflicts.
 __host__ __device__ constexpr int weight_floats(int units) { return (units + 7) / 8 * 128; }
 __device__ __forceinline__ int weight_at(int unit) { return (unit >> 3) * 128 + (unit & 7) * 4; }
@@ -194,8 +193,9 @@ __device__ __forceinline__ void fill_weights(const RopeParams& p, float* to) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const int at = h * p.hd + channel_of<HALF>(q, e / 2 % 4, e & 1, e / 8);
-      to[weight_at(i) + e / 4 * 32 + e % 4] = p.weight_fp32 ? __ldg(static_cast<const float*>(p.weight) + at)
-                                                          : widen16<FP16>(__ldg(static_cast<const uint16_t*>(p.weight) + at)).x;
+      to[weight_at(i) + e / 4 * 32 + e % 4] = !p.weight       ? 1.0f
+                                              : p.weight_fp32 ? __ldg(static_cast<const float*>(p.weight) + at)
+                                                              : widen16<FP16>(__ldg(static_cast<const uint16_t*>(p.weight) + at)).x;
     }
   }
 }
@@ -241,9 +241,9 @@ __device__ __forceinline__ Turn load_turn(const RopeParams& p, const Place& q, c
 }
 __device__ __forceinline__ uint64_t negated(uint64_t v) { return v ^ 0x8000000080000000ull; }
 
-// The pairs turned by their angles (SIGN -1: turned back). Pairs that pass (only where the
-// configuration has some) are put back, or a NaN would enter its partner.
-template <bool HALF, int SIGN>
+// The pairs turned by their angles (SIGN -1: turned back). PASS: some pairs of a head pass, and
+// are put back, or a NaN would enter its partner.
+template <bool HALF, bool PASS, int SIGN>
 __device__ __forceinline__ void turn(const RopeParams& p, const Place& q, const Turn& t, uint64_t (&first)[4], uint64_t (&second)[4]) {
   using namespace fused_norm_impl;
   uint64_t x[4], y[4];
@@ -253,7 +253,7 @@ __device__ __forceinline__ void turn(const RopeParams& p, const Place& q, const 
     x[j] = fma2(second[j], SIGN > 0 ? n : t.s[j], mul2(first[j], t.c[j]));
     y[j] = fma2(first[j], SIGN > 0 ? t.s[j] : n, mul2(second[j], t.c[j]));
   }
-  if (p.passes) {
+  if (PASS) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int pair = (j < 2 ? q.pairA : q.pairB) + 2 * (j & 1);
@@ -377,7 +377,7 @@ inline size_t forward_shared_bytes(int rows_per_cta, int hd, int weights) {
   return sizeof(ForwardShared) + ((size_t)2 * rows_per_cta * hd + weights) * sizeof(float);
 }
 
-template <bool FP16, int NH, int NORM, bool HALF>
+template <bool FP16, int NH, int NORM, bool HALF, bool PASS>
 __global__ void __launch_bounds__(kForwardThreads, 1) rope_norm_rows(const __grid_constant__ RopeParams p) {
   using namespace fused_norm_impl;
   extern __shared__ __align__(16) unsigned char raw[];
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) rope_norm_rows(const __gri
   float* const tables = reinterpret_cast<float*>(raw + sizeof(ForwardShared)) + (size_t)slot * p.hd;
   for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) sh.turns[i] = p.turns[i], sh.axis[i] = p.axis[i];
   float* const weights = reinterpret_cast<float*>(raw + sizeof(ForwardShared)) + (size_t)2 * R * p.hd;
-  if (NORM != BO_NORM_NONE) fill_weights<FP16, HALF>(p, weights);  // nothing without a weight
+  if (NORM != BO_NORM_NONE) fill_weights<FP16, HALF>(p, weights);
   __syncthreads();
 
   // Heads of a pass over the row: NH of each lane group of each warp; a norm over all heads
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) rope_norm_rows(const __gri
       const int n_next = last ? (more ? n0 : 0) : live ? heads_from(first + per_pass) : 0;
 #pragma unroll
       for (int k = 0; k < NH; ++k) {
-        const bool mine = k < n;
+        // What a thread without this head computes is not stored.
         uint64_t x[4], y[4];
         if (NORM == BO_NORM_HEAD) {
           split<FP16, HALF>(a[k], b[k], x, y);
@@ -498,26 +498,26 @@ __global__ void __launch_bounds__(kForwardThreads, 1) rope_norm_rows(const __gri
           for (int j = 0; j < 4; ++j) s[0] = fma2(x[j], x[j], s[0]), s[1] = fma2(y[j], y[j], s[1]);
           const float ss = lanes_sum(q.owns ? sum_of(add2(s[0], s[1])) : 0.0f, p.W);
           rho = rsqrtf(fmaf(ss, p.inv_n, p.eps));
-          const bool odd = mine && !in_range(ss);
+          const bool odd = k < n && !in_range(ss);
           if (__any_sync(0xFFFFFFFFu, odd)) {
             double e = 0.0;
             const uint16_t* v = xr + (first + k * p.G) * p.x.sh;
-            if (mine) e = exact_squares<FP16>(v + q.offA) + exact_squares<FP16>(v + q.offB);
+            if (k < n) e = exact_squares<FP16>(v + q.offA) + exact_squares<FP16>(v + q.offB);
             e = lanes_sum(e, p.W);
             if (odd) rho = (float)rsqrt(e * p.inv_n64 + p.eps64);
           }
         }
-        if (mine) {
-          split<FP16, HALF>(here(a[k]), here(b[k]), x, y);
-          if (NORM != BO_NORM_NONE) {
+        split<FP16, HALF>(here(a[k]), here(b[k]), x, y);
+        if (NORM != BO_NORM_NONE) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = mul2(x[j], pk2(rho, rho)), y[j] = mul2(y[j], pk2(rho, rho));
-            if (p.weight) weigh(weights + weight_at(unit), x, y);
-          }
-          turn<HALF, 1>(p, q, turns, x, y);
-          uint4 oa, ob;
-          join<FP16, HALF>(x, y, oa, ob);
-          if (NORM == BO_NORM_NONE && p.passes) keep_passing<HALF>(p, q, a[k], b[k], oa, ob);  // a NaN keeps its bits too
+          for (int j = 0; j < 4; ++j) x[j] = mul2(x[j], pk2(rho, rho)), y[j] = mul2(y[j], pk2(rho, rho));
+          weigh(weights + weight_at(min(unit, p.weight_units - 1)), x, y);
+        }
+        turn<HALF, PASS && NORM != BO_NORM_NONE, 1>(p, q, turns, x, y);
+        uint4 oa, ob;
+        join<FP16, HALF>(x, y, oa, ob);
+        if (NORM == BO_NORM_NONE && PASS) keep_passing<HALF>(p, q, a[k], b[k], oa, ob);  // a NaN keeps its bits too
+        if (k < n) {
           __stcs(reinterpret_cast<uint4*>(to), oa);
           __stcs(reinterpret_cast<uint4*>(to + apart), ob);
         }
@@ -545,12 +545,12 @@ struct Stage {
 };
 
 // A head's sums of x^2 and of w dn x over this thread's channels in fp64, for the rare rows.
-template <bool FP16, bool HALF>
+template <bool FP16, bool HALF, bool PASS>
 __device__ __noinline__ double2 exact_sums(const RopeParams& p, const Place& q, const float* table, const Stage& st, int k, const float* weight) {
   uint64_t x[2][4], d[2][4];
   split<FP16, HALF>(*st.at(k, 0), *st.at(k, 1), x[0], x[1]);
   split<FP16, HALF>(*st.at(k, 2), *st.at(k, 3), d[0], d[1]);
-  turn<HALF, -1>(p, q, load_turn(p, q, table), d[0], d[1]);
+  turn<HALF, PASS, -1>(p, q, load_turn(p, q, table), d[0], d[1]);
   double2 r = make_double2(0.0, 0.0);
   for (int i = 0; i < 2; ++i)
     for (int j = 0; j < 4; ++j) {
@@ -565,8 +565,9 @@ __device__ __noinline__ double2 exact_sums(const RopeParams& p, const Place& q, 
   return r;
 }
 
-__device__ __forceinline__ void copy_async(uint4* to, const uint16_t* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+// 16 bytes, or (bytes = 0) zeros without reading.
+__device__ __forceinline__ void copy_async(uint4* to, const uint16_t* from, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(bytes) : "memory");
 }
 
 // Shared memory of a CTA: the frequency table, sums; then three tables of cos and sin per row
@@ -588,8 +589,10 @@ inline size_t backward_shared_bytes(int rows_per_cta, int hd, int weights, int t
 }
 static_assert(sizeof(BackwardShared) % 16 == 0, "what follows is 16-byte aligned");
 
-// NORM: over the head or over all. DW: the kernel sums dweight's partials too.
-template <bool FP16, int NH, int NORM, bool HALF, bool DW>
+// NORM: over the head or over all. DW: there is a weight, whose gradient's partials the kernel
+// sums. Heads that a thread does not have, and rows past the last, are zeros in shared memory:
+// all arithmetic is unconditional, so that the heads' instructions mix.
+template <bool FP16, int NH, int NORM, bool HALF, bool DW, bool PASS>
 __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) rope_norm_gradient(const __grid_constant__ RopeParams p) {
   using namespace fused_norm_impl;
   extern __shared__ __align__(16) unsigned char raw[];
@@ -604,22 +607,23 @@ __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) 
   for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) sh.turns[i] = p.turns[i], sh.axis[i] = p.axis[i];
   fill_weights<FP16, HALF>(p, weights);
   __syncthreads();
-  auto weight = [&](int k) { return weights + weight_at((q.g + k * p.G) * p.weight_sh + q.u); };
+  const int apart = q.offB - q.offA;
+  auto weight = [&](int k) { return weights + weight_at(min((q.g + k * p.G) * p.weight_sh + q.u, p.weight_units - 1)); };
   auto table = [&](int buf) { return tables + (size_t)(buf * R + slot) * p.hd; };
   auto stage = [&](int buf) { return Stage{stages + (size_t)buf * NH * 4 * blockDim.x, (int)blockDim.x}; };
   auto has = [&](int k) { return q.owns && q.g + k * p.G < p.H; };
   auto fetch = [&](const RowAt& at, bool live, int buf) {
-    if (live) {
-      const Stage st = stage(buf);
-      const uint16_t *x = row_ptr(p.x, at) + q.g * p.x.sh, *d = row_ptr(p.dy, at) + q.g * p.dy.sh;
+    const Stage st = stage(buf);
+    const uint16_t* x = live ? row_ptr(p.x, at) + (q.g * p.x.sh + q.offA) : p.x.ptr;
+    const uint16_t* d = live ? row_ptr(p.dy, at) + (q.g * p.dy.sh + q.offA) : p.dy.ptr;
 #pragma unroll
-      for (int k = 0; k < NH; ++k, x += p.G * p.x.sh, d += p.G * p.dy.sh) {
-        if (!has(k)) continue;
-        copy_async(st.at(k, 0), x + q.offA);
-        copy_async(st.at(k, 1), x + q.offB);
-        copy_async(st.at(k, 2), d + q.offA);
-        copy_async(st.at(k, 3), d + q.offB);
-      }
+    for (int k = 0; k < NH; ++k) {
+      const uint32_t bytes = live && has(k) ? 16 : 0;
+      copy_async(st.at(k, 0), x, bytes);
+      copy_async(st.at(k, 1), x + apart, bytes);
+      copy_async(st.at(k, 2), d, bytes);
+      copy_async(st.at(k, 3), d + apart, bytes);
+      x += p.G * p.x.sh, d += p.G * p.dy.sh;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -636,21 +640,20 @@ __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) 
   auto begin = [&](const Turn& turns, const Stage& st, int k) {
     uint64_t x[4], y[4], sx[2] = {0, 0}, sg[2] = {0, 0};
     split<FP16, HALF>(*st.at(k, 2), *st.at(k, 3), dx[k], dy[k]);
-    turn<HALF, -1>(p, q, turns, dx[k], dy[k]);
+    turn<HALF, PASS, -1>(p, q, turns, dx[k], dy[k]);
     split<FP16, HALF>(*st.at(k, 0), *st.at(k, 1), x, y);
 #pragma unroll
     for (int j = 0; j < 4; ++j) sx[0] = fma2(x[j], x[j], sx[0]), sx[1] = fma2(y[j], y[j], sx[1]);
     uint64_t gx[4], gy[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) gx[j] = dx[k][j], gy[j] = dy[k][j];
-    if (p.weight) weigh(weight(k), gx, gy);
+    if (DW) weigh(weight(k), gx, gy);
 #pragma unroll
     for (int j = 0; j < 4; ++j) sg[0] = fma2(gx[j], x[j], sg[0]), sg[1] = fma2(gy[j], y[j], sg[1]);
     return make_float2(sum_of(add2(sx[0], sx[1])), sum_of(add2(sg[0], sg[1])));
   };
   // The output of head k, and its part of dweight; m = mean(w dn x) rho.
-  auto finish = [&](const Stage& st, uint16_t* ob, int k, float rho, float m) {
-    const int h = q.g + k * p.G;
+  auto finish = [&](const Stage& st, uint16_t* ob, bool store, int k, float rho, float m) {
     const uint64_t rr = pk2(rho, rho), mm = pk2(-m, -m);
     uint64_t x[4], y[4];
     split<FP16, HALF>(*st.at(k, 0), *st.at(k, 1), x, y);
@@ -661,14 +664,16 @@ __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) 
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[j] = fma2(dx[k][j], x[j], s[j]), s[4 + j] = fma2(dy[k][j], y[j], s[4 + j]);
     }
-    if (p.weight) weigh(weight(k), dx[k], dy[k]);
+    if (DW) weigh(weight(k), dx[k], dy[k]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = mul2(rr, fma2(x[j], mm, dx[k][j])), y[j] = mul2(rr, fma2(y[j], mm, dy[k][j]));
     uint4 va, vb;
     join<FP16, HALF>(x, y, va, vb);
-    uint16_t* const to = ob + here(h) * p.out.sh;
-    __stcs(reinterpret_cast<uint4*>(to + q.offA), va);
-    __stcs(reinterpret_cast<uint4*>(to + q.offB), vb);
+    if (store && has(k)) {
+      uint16_t* const to = ob + (here(q.g + k * p.G) * p.out.sh + q.offA);
+      __stcs(reinterpret_cast<uint4*>(to), va);
+      __stcs(reinterpret_cast<uint4*>(to + apart), vb);
+    }
   };
   // Sums that fp32 does not hold.
   auto outside = [](float xx, float gx) { return !(in_range(xx) && fabsf(gx) <= 0x1p+100f); };
@@ -709,11 +714,10 @@ __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) 
     float2 all = make_float2(0.0f, 0.0f);
     if (NORM == BO_NORM_ALL) {
 #pragma unroll
-      for (int k = 0; k < NH; ++k)
-        if (live && has(k)) {
-          const float2 s = begin(turns, st, k);
-          all.x += s.x, all.y += s.y;
-        }
+      for (int k = 0; k < NH; ++k) {
+        const float2 s = begin(turns, st, k);
+        all.x += s.x, all.y += s.y;
+      }
       all.x = lanes_sum(all.x, wide ? 32 : T);
       all.y = lanes_sum(all.y, wide ? 32 : T);
       if (wide && (t & 31) == 0) sh.sums[buf][t >> 5] = all;
@@ -727,15 +731,14 @@ __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) 
     if (NORM == BO_NORM_HEAD) {
 #pragma unroll
       for (int k = 0; k < NH; ++k) {
-        float2 s = make_float2(0.0f, 0.0f);
+        float2 s = begin(turns, st, k);
         const bool mine = live && has(k);
-        if (mine) s = begin(turns, st, k);
         s.x = lanes_sum(s.x, p.W);
         s.y = lanes_sum(s.y, p.W);
         float rho = rsqrtf(fmaf(s.x, p.inv_n, p.eps)), m = s.y * p.inv_n * rho;
         if (__any_sync(0xFFFFFFFFu, mine && outside(s.x, s.y))) {
           double2 e = make_double2(0.0, 0.0);
-          if (mine) e = exact_sums<FP16, HALF>(p, q, table(buf), st, k, weight(k));
+          if (mine) e = exact_sums<FP16, HALF, PASS>(p, q, table(buf), st, k, weight(k));
           e.x = lanes_sum(e.x, p.W);
           e.y = lanes_sum(e.y, p.W);
           if (outside(s.x, s.y)) {
@@ -743,7 +746,7 @@ __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) 
             rho = (float)f, m = (float)(e.y * p.inv_n64 * f);
           }
         }
-        if (mine) finish(st, ob, k, rho, m);
+        finish(st, ob, live, k, mine ? rho : 0.0f, mine ? m : 0.0f);
       }
     } else {
       if (wide) {
@@ -760,7 +763,7 @@ __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) 
 #pragma unroll 1
         for (int k = 0; k < NH; ++k)
           if (live && has(k)) {
-            const double2 one = exact_sums<FP16, HALF>(p, q, table(buf), st, k, weight(k));
+            const double2 one = exact_sums<FP16, HALF, PASS>(p, q, table(buf), st, k, weight(k));
             e.x += one.x, e.y += one.y;
           }
         e.x = lanes_sum(e.x, wide ? 32 : T);
@@ -777,9 +780,9 @@ __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) 
           rho = (float)f, m = (float)(e.y * p.inv_n64 * f);
         }
       }
+      if (!live) rho = m = 0.0f;  // zeros over zero
 #pragma unroll
-      for (int k = 0; k < NH; ++k)
-        if (live && has(k)) finish(st, ob, k, rho, m);
+      for (int k = 0; k < NH; ++k) finish(st, ob, live, k, rho, m);
     }
     at = at1, at1 = at2;
   }
@@ -837,43 +840,52 @@ using RopeKernel = void (*)(RopeParams);
 // Kernels for (threads' heads, norm, pairing); the two element types are compiled in files of
 // their own. Forward: 1, 2 or 4 heads, and 6 or 10 for a norm over all; gradient: 1, 2 or 4.
 template <bool FP16>
-RopeKernel pick_rope(int nh, int norm, bool half);
+RopeKernel pick_rope(int nh, int norm, bool half, bool pass);
 template <bool FP16>
-RopeKernel pick_rope_gradient(int nh, int norm, bool half, bool dw);
-extern template RopeKernel pick_rope<false>(int, int, bool);
-extern template RopeKernel pick_rope<true>(int, int, bool);
-extern template RopeKernel pick_rope_gradient<false>(int, int, bool, bool);
-extern template RopeKernel pick_rope_gradient<true>(int, int, bool, bool);
+RopeKernel pick_rope_gradient(int nh, int norm, bool half, bool dw, bool pass);
+extern template RopeKernel pick_rope<false>(int, int, bool, bool);
+extern template RopeKernel pick_rope<true>(int, int, bool, bool);
+extern template RopeKernel pick_rope_gradient<false>(int, int, bool, bool, bool);
+extern template RopeKernel pick_rope_gradient<true>(int, int, bool, bool, bool);
 
-template <bool FP16, int NORM, bool HALF>
+template <bool FP16, int NORM, bool HALF, bool PASS>
 RopeKernel pick_rope_heads(int nh) {
   if constexpr (NORM == BO_NORM_ALL) {
-    if (nh == 6) return rope_norm_rows<FP16, 6, NORM, HALF>;
-    if (nh == 10) return rope_norm_rows<FP16, 10, NORM, HALF>;
+    if (nh == 6) return rope_norm_rows<FP16, 6, NORM, HALF, PASS>;
+    if (nh == 10) return rope_norm_rows<FP16, 10, NORM, HALF, PASS>;
   }
-  return nh == 1 ? rope_norm_rows<FP16, 1, NORM, HALF> : nh == 2 ? rope_norm_rows<FP16, 2, NORM, HALF> : rope_norm_rows<FP16, 4, NORM, HALF>;
-}
-template <bool FP16, int NORM, bool HALF, bool DW>
-RopeKernel pick_rope_gradient_heads(int nh) {
-  return nh == 1   ? rope_norm_gradient<FP16, 1, NORM, HALF, DW>
-         : nh == 2 ? rope_norm_gradient<FP16, 2, NORM, HALF, DW>
-                   : rope_norm_gradient<FP16, 4, NORM, HALF, DW>;
-}
-template <bool FP16>
-RopeKernel pick_rope(int nh, int norm, bool half) {
-  if (norm == BO_NORM_NONE) return half ? pick_rope_heads<FP16, BO_NORM_NONE, true>(nh) : pick_rope_heads<FP16, BO_NORM_NONE, false>(nh);
-  if (norm == BO_NORM_HEAD) return half ? pick_rope_heads<FP16, BO_NORM_HEAD, true>(nh) : pick_rope_heads<FP16, BO_NORM_HEAD, false>(nh);
-  return half ? pick_rope_heads<FP16, BO_NORM_ALL, true>(nh) : pick_rope_heads<FP16, BO_NORM_ALL, false>(nh);
+  return nh == 1   ? rope_norm_rows<FP16, 1, NORM, HALF, PASS>
+         : nh == 2 ? rope_norm_rows<FP16, 2, NORM, HALF, PASS>
+                   : rope_norm_rows<FP16, 4, NORM, HALF, PASS>;
 }
 template <bool FP16, int NORM>
-RopeKernel pick_rope_gradient_norm(int nh, bool half, bool dw) {
-  if (half) return dw ? pick_rope_gradient_heads<FP16, NORM, true, true>(nh) : pick_rope_gradient_heads<FP16, NORM, true, false>(nh);
-  return dw ? pick_rope_gradient_heads<FP16, NORM, false, true>(nh) : pick_rope_gradient_heads<FP16, NORM, false, false>(nh);
+RopeKernel pick_rope_norm(int nh, bool half, bool pass) {
+  if (half) return pass ? pick_rope_heads<FP16, NORM, true, true>(nh) : pick_rope_heads<FP16, NORM, true, false>(nh);
+  return pass ? pick_rope_heads<FP16, NORM, false, true>(nh) : pick_rope_heads<FP16, NORM, false, false>(nh);
 }
 template <bool FP16>
-RopeKernel pick_rope_gradient(int nh, int norm, bool half, bool dw) {
-  return norm == BO_NORM_HEAD ? pick_rope_gradient_norm<FP16, BO_NORM_HEAD>(nh, half, dw)
-                              : pick_rope_gradient_norm<FP16, BO_NORM_ALL>(nh, half, dw);
+RopeKernel pick_rope(int nh, int norm, bool half, bool pass) {
+  return norm == BO_NORM_NONE   ? pick_rope_norm<FP16, BO_NORM_NONE>(nh, half, pass)
+         : norm == BO_NORM_HEAD ? pick_rope_norm<FP16, BO_NORM_HEAD>(nh, half, pass)
+                                : pick_rope_norm<FP16, BO_NORM_ALL>(nh, half, pass);
+}
+
+template <bool FP16, int NORM, bool HALF, bool DW, bool PASS>
+RopeKernel pick_rope_gradient_heads(int nh) {
+  return nh == 1   ? rope_norm_gradient<FP16, 1, NORM, HALF, DW, PASS>
+         : nh == 2 ? rope_norm_gradient<FP16, 2, NORM, HALF, DW, PASS>
+                   : rope_norm_gradient<FP16, 4, NORM, HALF, DW, PASS>;
+}
+template <bool FP16, int NORM, bool HALF>
+RopeKernel pick_rope_gradient_half(int nh, bool dw, bool pass) {
+  if (dw) return pass ? pick_rope_gradient_heads<FP16, NORM, HALF, true, true>(nh) : pick_rope_gradient_heads<FP16, NORM, HALF, true, false>(nh);
+  return pass ? pick_rope_gradient_heads<FP16, NORM, HALF, false, true>(nh) : pick_rope_gradient_heads<FP16, NORM, HALF, false, false>(nh);
+}
+template <bool FP16>
+RopeKernel pick_rope_gradient(int nh, int norm, bool half, bool dw, bool pass) {
+  if (norm == BO_NORM_HEAD)
+    return half ? pick_rope_gradient_half<FP16, BO_NORM_HEAD, true>(nh, dw, pass) : pick_rope_gradient_half<FP16, BO_NORM_HEAD, false>(nh, dw, pass);
+  return half ? pick_rope_gradient_half<FP16, BO_NORM_ALL, true>(nh, dw, pass) : pick_rope_gradient_half<FP16, BO_NORM_ALL, false>(nh, dw, pass);
 }
 
 }  // namespace block_ops
