@@ -17,7 +17,8 @@
 
 #include <cuda_fp8.h>
 
-#include "rope_norm_kernel.cuh"
+#include "../../../include/block_ops.h"
+#include "elements.cuh"
 #include "tcgen05.cuh"
 
 namespace block_ops {

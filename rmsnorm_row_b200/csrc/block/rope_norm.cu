@@ -82,7 +82,7 @@ RopeShape backward_shape(int H, int hd) {
   RopeShape s{W, 0, 0, 0, 0, nullptr, 0, 0};
   for (int nh : {2, 1, 4}) {
     const int T = ((H + nh - 1) / nh * W + 31) / 32 * 32;
-    if (T <= (nh == 4 ? kRopeThreads : kGradientThreads) && (s.T == 0 || T * nh < s.T * s.nh)) s.T = T, s.nh = nh;
+    if (T <= kRopeThreads && (s.T == 0 || T * nh < s.T * s.nh)) s.T = T, s.nh = nh;
   }
   s.G = s.T / W;
   s.rows_per_cta = s.T > 32 ? 1 : kSharedRows / s.T;
@@ -330,7 +330,7 @@ fn_status rope_norm_create(rope_norm_t* out, const rn_config* cfg) {
     } else if (c.norm != BO_NORM_NONE) {
       s.kernel = c.dtype == BO_FP16 ? pick_rope_gradient<true>(s.nh, c.norm, c.half_pairs, sums_dweight(c), pass)
                                     : pick_rope_gradient<false>(s.nh, c.norm, c.half_pairs, sums_dweight(c), pass);
-      for (s.stages = kStages; s.stages >= 1; --s.stages) {
+      for (s.stages = 2; s.stages >= 1; --s.stages) {
         s.smem = backward_shared_bytes(s.rows_per_cta, c.head_dim, weights, s.T * s.rows_per_cta, s.nh, s.stages);
         if (s.smem <= kMaxShared) break;
       }

@@ -19,24 +19,15 @@
 // neighbouring vectors. A norm over the head is a shuffle inside W lanes.
 #pragma once
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-#include <stdint.h>
-
-#include "../fused_norm_kernel.cuh"
 #include "../../../include/block_ops.h"
+#include "elements.cuh"
 
 namespace block_ops {
-
-using fused_norm_impl::DivU32;
-using fused_norm_impl::div_u32;
 
 constexpr int kMaxPairs = 256;      // of a head
 constexpr int kRopeThreads = 512;   // of a CTA, at most
 constexpr int kForwardThreads = 384;  // of a forward CTA: 168 registers hold a lane's ten heads
 constexpr int kSharedRows = 128;    // threads of a CTA whose rows take 32 lanes or fewer
-constexpr int kGradientThreads = 384; // of a gradient CTA with one or two heads to a thread
 constexpr int kMaxPartials = 1024;  // CTAs that sum dweight
 
 struct RopeRows {
@@ -55,7 +46,7 @@ struct RopeParams {
   DivU32 div_L;
   int H, hd, units, pairs;  // units of a head (hd / 16), pairs that turn
   int W, T, G;              // lanes of a head, threads of a row, lane groups (of a warp, in the forward kernel)
-  int stages;               // rows of the gradient kernel in shared memory: 1 to 3
+  int stages;               // rows of the gradient kernel in shared memory: 2 or 1
   float sign;               // -1 turns the other way
   int index64, weight_fp32;
   int weight_sh, weight_units;  // units from a head's weights to the next (0: one head's); units of it (0: none)
@@ -64,44 +55,6 @@ struct RopeParams {
   double turns[kMaxPairs];    // freq / 2 pi
   uint8_t axis[kMaxPairs];
 };
-
-// ---- element types --------------------------------------------------------------------------
-
-template <bool FP16>
-__device__ __forceinline__ float2 widen16(uint32_t u) {
-  if (FP16) {
-    __half2 h;
-    memcpy(&h, &u, 4);
-    return __half22float2(h);
-  }
-  return make_float2(fused_norm_impl::lo_f(u), fused_norm_impl::hi_f(u));
-}
-
-template <bool FP16>
-__device__ __forceinline__ uint32_t pack16(float a, float b) {
-  if (FP16) {
-    const __half2 h = __floats2half2_rn(a, b);
-    uint32_t u;
-    memcpy(&u, &h, 4);
-    return u;
-  }
-  return fused_norm_impl::pack_rn(a, b);
-}
-
-template <bool FP16>
-__device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 e = widen16<FP16>(fused_norm_impl::word(v, i));
-    f[2 * i] = e.x, f[2 * i + 1] = e.y;
-  }
-}
-
-template <bool FP16>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack16<FP16>(f[0], f[1]), pack16<FP16>(f[2], f[3]), pack16<FP16>(f[4], f[5]),
-                    pack16<FP16>(f[6], f[7]));
-}
 
 // ---- one thread's place in a row ---------------------------------------------------------------
 
@@ -366,7 +319,7 @@ __device__ __forceinline__ double exact_squares(const uint16_t* at) {
 // heads. Each head's registers take the next row's vectors as soon as its output is stored, so
 // loads are in flight while the row is worked on.
 
-struct ForwardShared {
+struct alignas(16) ForwardShared {
   double turns[kMaxPairs];
   float sums[2][kForwardThreads / 32][32];
   double sums64[kForwardThreads / 32];
@@ -533,8 +486,10 @@ __global__ void __launch_bounds__(kForwardThreads, 1) rope_norm_rows(const __gri
 //
 // One row per CTA turn (rows of 32 lanes or fewer share warps) with NH heads to a thread, since
 // a thread also keeps dn between the sums and the output, and the sums of dweight over its rows.
-// Each thread copies its own vectors of the next two rows to shared memory while it works on the
-// present one, so no registers wait for loads and nobody else has to be waited for.
+// Each thread copies its own vectors of the next row to shared memory while it works on the
+// present one, so no registers wait for loads and nobody else has to be waited for. 128 registers and two
+// stages let three CTAs of a row of 5120 channels run side by side (two with 168 registers or a
+// third stage): 1.08 against 1.24 ms over 176400 tokens.
 
 // A thread's own two vectors of a head, in shared memory: x's, then grad's. One stage holds all
 // heads of a thread; vectors of neighbouring threads are neighbours.
@@ -571,18 +526,18 @@ __device__ __forceinline__ void copy_async(uint4* to, const uint16_t* from, uint
 }
 
 // Shared memory of a CTA: the frequency table, sums; then three tables of cos and sin per row
-// slot, the weights, and the stages of rows (three, or as many as fit). A row's table is written before the barrier of the row
+// slot, the weights, and the stages of rows (two, or one where two do not fit). A row's table is written before the barrier of the row
 // ahead of it and read up to the barrier of the row behind it, so its buffer comes round again
 // at the third row.
-constexpr int kStages = 3;
-struct BackwardShared {
+constexpr int kTables = 3;
+struct alignas(16) BackwardShared {
   double turns[kMaxPairs];
   double sums64[2][kRopeThreads / 32];
-  float2 sums[kStages][kRopeThreads / 32];
+  float2 sums[kTables][kRopeThreads / 32];
   uint8_t axis[kMaxPairs];
 };
 __host__ __device__ inline size_t backward_tables_bytes(int rows_per_cta, int hd) {
-  return (size_t)kStages * rows_per_cta * hd * sizeof(float);
+  return (size_t)kTables * rows_per_cta * hd * sizeof(float);
 }
 inline size_t backward_shared_bytes(int rows_per_cta, int hd, int weights, int threads, int nh, int stages) {
   return sizeof(BackwardShared) + backward_tables_bytes(rows_per_cta, hd) + (size_t)weights * sizeof(float) + (size_t)stages * threads * nh * 4 * 16;
@@ -593,7 +548,7 @@ static_assert(sizeof(BackwardShared) % 16 == 0, "what follows is 16-byte aligned
 // sums. Heads that a thread does not have, and rows past the last, are zeros in shared memory:
 // all arithmetic is unconditional, so that the heads' instructions mix.
 template <bool FP16, int NH, int NORM, bool HALF, bool DW, bool PASS>
-__global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) rope_norm_gradient(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 1) rope_norm_gradient(const __grid_constant__ RopeParams p) {
   using namespace fused_norm_impl;
   extern __shared__ __align__(16) unsigned char raw[];
   BackwardShared& sh = *reinterpret_cast<BackwardShared*>(raw);
@@ -602,7 +557,7 @@ __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) 
   const int slot = threadIdx.x / T, t = threadIdx.x - slot * T;
   const bool wide = T > 32;
   const Place q = place_of<HALF>(p, t);
-  float* const weights = tables + (size_t)kStages * R * p.hd;
+  float* const weights = tables + (size_t)kTables * R * p.hd;
   uint4* const stages = reinterpret_cast<uint4*>(weights + weight_floats(p.weight_units)) + threadIdx.x;
   for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) sh.turns[i] = p.turns[i], sh.axis[i] = p.axis[i];
   fill_weights<FP16, HALF>(p, weights);
@@ -680,9 +635,8 @@ __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) 
 
   const uint32_t step = gridDim.x * R;
   uint32_t base = blockIdx.x * R;
-  RowAt at = row_at(p, base + slot), at1 = row_at(p, base + slot + step);
+  RowAt at = row_at(p, base + slot), at1 = row_at(p, base + slot + step);  // rows + 2 step < 2^32: the host bounds both
   if (p.stages > 1) fetch(at, base + slot < p.rows, 0);
-  if (p.stages > 2) fetch(at1, base + slot + step < p.rows, 1);  // rows + 2 step < 2^32: the host bounds both
   Angles angles{sh.turns, sh.axis, make_int2(0, 0)};
   if (base + slot < p.rows) {
     angles.read_ahead(p, at, t);
@@ -692,7 +646,7 @@ __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) 
   if (wide) __syncthreads();
   else __syncwarp();
 
-  for (int buf = 0, ahead = 1, now = 0; base < p.rows; base += step, buf = ahead, ahead = ahead == kStages - 1 ? 0 : ahead + 1,
+  for (int buf = 0, ahead = 1, now = 0; base < p.rows; base += step, buf = ahead, ahead = ahead == kTables - 1 ? 0 : ahead + 1,
            now = now == p.stages - 1 ? 0 : now + 1) {
     const uint32_t row = base + slot;
     const bool live = row < p.rows;
@@ -700,10 +654,7 @@ __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) 
     const RowAt at2 = row_at(p, row + 2 * step);
     const Turn turns = load_turn(p, q, table(buf));
     // the stage before this one is free; then this row's vectors are here
-    if (p.stages == 3) {
-      fetch(at2, row + 2 * step < p.rows, now == 0 ? 2 : now - 1);
-      asm volatile("cp.async.wait_group 2;" ::: "memory");
-    } else if (p.stages == 2) {
+    if (p.stages == 2) {
       fetch(at1, row + step < p.rows, now ^ 1);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
     } else {
@@ -810,28 +761,31 @@ __global__ void __launch_bounds__(NH == 4 ? kRopeThreads : kGradientThreads, 1) 
   // through the first stage (every thread is past its rows, and its copies have landed).
   asm volatile("cp.async.wait_all;" ::: "memory");
   const int span = NORM == BO_NORM_ALL ? T : p.W;
-  float v[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    v[i] = value(0, i);
-    for (int o = span; o < 32; o <<= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
-  }
   float* const sums = reinterpret_cast<float*>(stages - threadIdx.x);  // 16 values of `span` lanes
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-    __syncthreads();
-    if ((int)(threadIdx.x >> 5) == w && (int)(threadIdx.x & 31) < span) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float& s = sums[i * 32 + (threadIdx.x & 31)];
-        s = (w ? s : 0.0f) + v[i];
+  for (int k = 0; k < NACC; ++k) {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      v[i] = value(k, i);
+      for (int o = span; o < 32; o <<= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+    }
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+      __syncthreads();
+      if ((int)(threadIdx.x >> 5) == w && (int)(threadIdx.x & 31) < span) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float& s = sums[i * 32 + (threadIdx.x & 31)];
+          s = (w ? s : 0.0f) + v[i];
+        }
       }
     }
-  }
-  __syncthreads();
-  if ((int)threadIdx.x < span && has(0)) {
-    float* o = part + (NORM == BO_NORM_ALL ? q.g * p.hd : 0);
+    __syncthreads();
+    if ((int)threadIdx.x < span && has(k)) {
+      float* o = part + (NORM == BO_NORM_ALL ? (q.g + k * p.G) * p.hd : 0);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[channel_of<HALF>(q, (i / 2) % 4, i & 1, i / 8)] = sums[i * 32 + threadIdx.x];
+      for (int i = 0; i < 16; ++i) o[channel_of<HALF>(q, (i / 2) % 4, i & 1, i / 8)] = sums[i * 32 + threadIdx.x];
+    }
   }
 }
 

@@ -170,6 +170,42 @@ def test_gradient_against_the_formula(case):
     check_backward(dx, dw, dy, x, pos, sections, w, **kw)
 
 
+# Every number of heads per thread and warps per row of both directions; rows whose stages fill
+# shared memory (48, 144, 432); two heads to a thread of a row that has one warp (6, 16).
+SHAPES = [
+    (2, 11, 6, 128, (22, 21, 21), BF, "all", F32, "interleaved", True, I32, 0),
+    (1, 700, 6, 128, (22, 21, 21), BF, "all", BF, "half", False, I32, 0),
+    (1, 9, 16, 64, (32,), BF, "all", HF, "half", False, I32, 0),
+    (1, 650, 16, 64, (30,), BF, "all", F32, "interleaved", False, I32, 0),
+    (1, 650, 24, 128, (22, 21, 21), BF, "all", BF, "interleaved", False, I32, 0),
+    (1, 600, 14, 128, (64,), HF, "all", HF, "half", False, I32, 0),
+    (2, 301, 30, 96, (16, 16, 16), HF, "all", F32, "half", True, I64, 7),
+    (1, 650, 48, 128, (64,), BF, "all", BF, "interleaved", False, I32, 0),
+    (1, 650, 128, 128, (56,), BF, "all", BF, "interleaved", False, I32, 0),
+    (1, 9, 289, 48, (24,), BF, "all", BF, "interleaved", False, I32, 0),
+    (1, 700, 105, 144, (40, 32), HF, "all", HF, "half", False, I32, 0),
+    (1, 9, 37, 432, (100, 100), BF, "all", F32, "interleaved", False, I32, 0),
+    (1, 650, 37, 432, (100, 108), BF, "head", F32, "half", False, I32, 0),
+    (1, 1000, 341, 48, (3,), BF, "head", BF, "interleaved", False, I32, 0),
+    (1, 650, 204, 80, (40,), HF, "none", None, "half", False, I32, 0),
+    (1, 650, 9, 64, (32,), BF, "head", BF, "interleaved", False, I32, 0),
+    (1, 650, 1024, 16, (8,), BF, "all", BF, "half", False, I32, 0),
+]
+
+
+@pytest.mark.parametrize("case", SHAPES, ids=ids)
+def test_launch_shapes(case):
+    dy, x, pos, sections, w, kw = make(case, 100)
+    if w is not None and w.dtype not in (x.dtype, F32):
+        w = w.to(x.dtype)
+    y = fn.rope_norm(x, pos, sections, w, **kw)
+    check_forward(y, x, pos, sections, w, **kw)
+    few = slice(x.shape[1] // 2, x.shape[1] // 2 + 3)  # few rows, in other launch shapes: the same bits
+    assert torch.equal(fn.rope_norm(x[:, few], pos[few], sections, w, **kw), y[:, few])
+    dx, dw = fn.rope_norm_backward(dy, x, pos, sections, w, **kw)
+    check_backward(dx, dw, dy, x, pos, sections, w, **kw)
+
+
 @pytest.mark.parametrize("case", [CASES[3], CASES[7], CASES[5]], ids=ids)
 def test_gradient_against_differences(case):
     """<dx, v> against central differences of the formula along v (an error of delta^2)."""
