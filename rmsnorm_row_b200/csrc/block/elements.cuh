@@ -43,4 +43,18 @@ __device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
   }
 }
 
+// The same value, which the compiler cannot trace: what depends on it is computed where it is
+// used, and not earlier into registers that then wait (addresses of ten heads for all rows, or
+// a row widened for its sum and kept for its output, took more registers than the row).
+__device__ __forceinline__ uint4 here(uint4 v) {
+  asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w));
+  return v;
+}
+template <typename V>
+__device__ __forceinline__ V here(V v) {
+  if constexpr (sizeof(V) == 8) asm volatile("" : "+l"(v));
+  else asm volatile("" : "+r"(v));
+  return v;
+}
+
 }  // namespace block_ops

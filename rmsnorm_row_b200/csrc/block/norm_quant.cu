@@ -6,21 +6,27 @@
 // row_scale = a / 448; q = e4m3(y 448 / a).
 //
 // Bound: HBM. A row moves 2 (x) + 2 (residual) + 2 (r) + 1 (q) bytes per element, plus 4 with
-// per-token modulation, against ~15 fp32 operations. The row therefore stays in registers
-// from its only read to its only write: as packed bf16 for the statistics, as fp32 from the
-// norm to the quantisation (the scale needs the whole row's maximum first).
+// per-token modulation. At the copy rate an SM has some 6000 instruction slots for a row of 5120
+// channels without modulation of its own, so instructions count too: arithmetic on fp32 pairs,
+// and what rows share is prepared once. The row stays in registers from its only read to its
+// only write, as fp32 (the scale needs the whole row's maximum before anything is quantised).
 //
 // Layout: thread t of the row's T threads owns the 16-byte vectors t, t + T, ... (every warp
-// access is 512 contiguous bytes). Rows of up to 1024 channels take one warp each, eight rows
-// to a CTA, and reduce through shuffles alone; longer rows take one CTA of T threads with NV
-// vectors each and one barrier per reduction (statistics, then the maximum).
+// access is 512 contiguous bytes), at most five. A row meets at two barriers, for its statistics
+// and its maximum; rows of one warp reduce through shuffles alone.
+//
+// Where no operand changes from token to token, CTAs are persistent (one per SM, its threads as
+// groups of T with a row each) and keep gate, weight (1 + scale) and bias (1 + scale) + shift of
+// their frame or batch in shared memory; the next row's vectors are requested as soon as this
+// one's are used. Otherwise, and for few rows, a group of T threads takes one row and reads its
+// operands with it. Both compute the same values in the same order.
 #include <cuda_fp8.h>
 
 #include <cmath>
 #include <cstring>
 #include <new>
 
-#include "../fused_norm_kernel.cuh"
+#include "elements.cuh"
 #include "host_checks.h"
 
 namespace block_ops {
@@ -40,42 +46,23 @@ struct QuantParams {
   uint32_t rows, L, tpf;
   DivU32 div_L, div_tpf;
   uint32_t vecs;  // D / 8
+  uint32_t chunk;    // rows of a CTA
+  uint32_t segment;  // rows with the same gate, scale and shift, from row 0 on
+  DivU32 div_segment;
   uint32_t stream_mask;
   uint32_t affine_fp32;
   double inv_d;  // 1 / D
   double eps;
 };
 
-constexpr int kMaxWarps = 16;  // of a row: T <= 512
-constexpr int kRowsPerCta = 8;  // rows of one warp each
+constexpr int kMaxWarps = 16;  // of a CTA
+constexpr int kMaxThreads = 32 * kMaxWarps;
+constexpr int kMaxVectors = 5;   // of a thread
 
-// Sums over the row's threads, the same value in each of them. `slot` is shared memory of a
-// CTA-wide row that nothing else has used since the last barrier.
-template <bool WARP_ROW>
-__device__ __forceinline__ double row_sum(double v, double* slot) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if (WARP_ROW) return v;
-  const int warps = blockDim.x >> 5;
-  if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double t = slot[0];
-  for (int w = 1; w < warps; ++w) t += slot[w];
-  return t;
-}
-
-// Bits of the largest |y| over the row's threads. Magnitudes order as unsigned integers, and
-// a NaN's lie above infinity's: a NaN anywhere makes the row's maximum a NaN.
-template <bool WARP_ROW>
-__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* slot) {
-  v = __reduce_max_sync(0xFFFFFFFFu, v);
-  if (WARP_ROW) return v;
-  const int warps = blockDim.x >> 5;
-  if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
-  __syncthreads();
-  uint32_t t = slot[0];
-  for (int w = 1; w < warps; ++w) t = max(t, slot[w]);
-  return t;
+// The largest of three magnitudes; a NaN stays.
+__device__ __forceinline__ float max_abs(float top, float a, float b) {
+  asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(a), "f"(b));
+  return top;
 }
 
 __device__ __forceinline__ uint64_t widen(uint32_t pair) { return pk2(lo_f(pair), hi_f(pair)); }
@@ -93,98 +80,113 @@ __device__ __forceinline__ void load_affine(const void* p, bool fp32, int j, uin
   }
 }
 
-template <int NV, bool IS_RMS, bool ROW_MOD, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? 32 * kRowsPerCta : 512)
-norm_quant_rows(const QuantParams p) {
-  __shared__ double sums[4][kMaxWarps];
-  __shared__ uint32_t tops[kMaxWarps];
-  const uint32_t row = WARP_ROW ? blockIdx.x * kRowsPerCta + threadIdx.y : blockIdx.x;
-  if (WARP_ROW && row >= p.rows) return;  // whole warps
-  const int tid = threadIdx.x, T = WARP_ROW ? 32 : blockDim.x;
+// y = n a + b of a vector: a = weight (1 + scale), b = bias (1 + scale) + shift.
+__device__ __forceinline__ void coefficients(const QuantParams& p, int j, bool modulated, const uint4& scale, const uint4& shift,
+                                             uint64_t (&a)[4], uint64_t (&b)[4]) {
+  const uint64_t one = pk2(1.0f, 1.0f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = one, b[i] = 0;
+  if (p.weight) load_affine(p.weight, p.affine_fp32, j, a);
+  if (p.bias) load_affine(p.bias, p.affine_fp32, j, b);
+  if (modulated) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t s = add2(widen(word(scale, i)), one);
+      a[i] = mul2(a[i], s);
+      b[i] = fma2(b[i], s, widen(word(shift, i)));
+    }
+  }
+}
+
+struct RowAt {
+  uint32_t b, l, f;
+};
+__device__ __forceinline__ RowAt row_at(const QuantParams& p, uint32_t row) {
   const uint32_t b = div_u32(row, p.div_L), l = row - b * p.L;
-  const uint32_t f = p.tpf > 0 ? div_u32(l, p.div_tpf) : 0u;
-  auto has = [&](int k) { return (uint32_t)(tid + k * T) < p.vecs; };
+  return RowAt{b, l, p.tpf > 0 ? div_u32(l, p.div_tpf) : 0u};
+}
+__device__ __forceinline__ const uint16_t* at_row(const uint16_t* base, int64_t sb, int64_t sf, int64_t sl, const RowAt& r) {
+  return base + (r.b * sb + r.f * sf + r.l * sl);
+}
 
-  // ---- the row: r = residual + gate x, or x; packed bf16 in v -------------------------
-  const uint16_t* xr = p.x + (b * p.x_sb + f * p.x_sf + l * p.x_sl);
-  uint4 v[NV];
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-    v[k] = has(k) ? load_vec(xr, tid + k * T, p.stream_mask & kX) : make_uint4(0, 0, 0, 0);
-  if (p.res) {
-    const uint16_t* rr = p.res + (b * p.res_sb + f * p.res_sf + l * p.res_sl);
-    uint16_t* ro = p.r + (b * p.r_sb + l * p.r_sl);
-    uint4 rv[NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      rv[k] = has(k) ? load_vec(rr, tid + k * T, p.stream_mask & kRes) : make_uint4(0, 0, 0, 0);
-    if (p.gate) {
-      const uint16_t* gr = p.gate + (b * p.gate_sb + f * p.gate_sf + l * p.gate_sl);
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (has(k)) v[k] = residual_vec<true>(rv[k], v[k], load_vec(gr, tid + k * T, p.stream_mask & kGate));
-    } else {
-#pragma unroll
-      for (int k = 0; k < NV; ++k) v[k] = residual_vec<false>(rv[k], v[k], v[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (has(k)) __stcs(reinterpret_cast<uint4*>(ro) + tid + k * T, v[k]);
+// Shared memory of a group: its warps' sums and maxima, of this row and the next by turns.
+struct GroupShared {
+  double sums[2][2][kMaxWarps];
+  double again[2][kMaxWarps];
+  float tops[2][kMaxWarps];
+};
+
+// A row's threads: T of them, in warps of their own.
+struct Group {
+  GroupShared* sh;
+  int id, tid, T;
+
+  __device__ __forceinline__ void meet() const {
+    if (T > 32) asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(T) : "memory");
+    else __syncwarp();
   }
-
-  // Modulation that changes from token to token is requested here, so that the statistics
-  // hide its latency; broadcast rows come from L1 where they are used.
-  const uint16_t* sr = p.scale ? p.scale + (b * p.scale_sb + f * p.scale_sf + l * p.scale_sl) : nullptr;
-  const uint16_t* tr = p.scale ? p.shift + (b * p.shift_sb + f * p.shift_sf + l * p.shift_sl) : nullptr;
-  uint4 sv[ROW_MOD ? NV : 1], tv[ROW_MOD ? NV : 1];
-  if (ROW_MOD) {
+  // The sum over the row's threads, the same value in each of them.
+  __device__ __forceinline__ double sum(double v, double* slot) const {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (has(k)) {
-        sv[k] = load_vec(sr, tid + k * T, p.stream_mask & kScale);
-        tv[k] = load_vec(tr, tid + k * T, p.stream_mask & kShift);
-      }
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (T == 32) return v;
+    if ((tid & 31) == 0) slot[tid >> 5] = v;
+    meet();
+    v = slot[0];
+    for (int w = 1; w < (T >> 5); ++w) v += slot[w];
+    return v;
   }
+  // Magnitudes order as unsigned integers, a NaN's above infinity's.
+  __device__ __forceinline__ float max(float v, float* slot) const {
+    uint32_t t = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v));
+    if (T == 32) return __uint_as_float(t);
+    if ((tid & 31) == 0) slot[tid >> 5] = __uint_as_float(t);
+    meet();
+    t = __float_as_uint(slot[0]);
+    for (int w = 1; w < (T >> 5); ++w) t = ::max(t, __float_as_uint(slot[w]));
+    return __uint_as_float(t);
+  }
+};
 
-  // ---- statistics: fp32 within a thread (at most 40 elements), fp64 across threads ------
-  // LayerNorm sums squares around the thread's own mean m, so nothing cancels in fp32:
-  // sum r^2 = sum (r - m)^2 + m (2 S - n m), joined in fp64. An error of S enters the
-  // variance only through its product with m - mu.
+struct Stats {
+  float rho, mu_hi, mu_lo;  // r - mu keeps fp32's precision
+};
+
+// fp32 within a thread (at most 40 elements), fp64 across threads. v(k, i): pair i of the thread's
+// vector k in fp32, zeros where it has none; `full`: it has its last one. `again`: the row in memory.
+// LayerNorm sums squares around the thread's own mean m, so nothing cancels in fp32:
+// sum r^2 = sum (r - m)^2 + m (2 S - n m), joined in fp64. An error of S enters the variance
+// only through its product with m - mu.
+template <int NV, bool IS_RMS, typename Values>
+__device__ __forceinline__ Stats statistics(const QuantParams& p, const Group& g, int parity, Values v, bool full, const uint4* again) {
   double mu = 0.0, var;
+  uint64_t acc[2] = {0, 0};
+  float a0, a1;
   if (IS_RMS) {
-    uint64_t acc[2] = {0, 0};
 #pragma unroll
-    for (int k = 0; k < NV; ++k)  // vectors past the row's end are zero
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint64_t e = widen(word(v[k], i));
-        acc[i & 1] = fma2(e, e, acc[i & 1]);
-      }
-    float a0, a1;
+      for (int i = 0; i < 4; ++i) acc[i & 1] = fma2(v(k, i), v(k, i), acc[i & 1]);
     upk2(add2(acc[0], acc[1]), a0, a1);
-    var = row_sum<WARP_ROW>((double)a0 + (double)a1, sums[0]) * p.inv_d;
+    var = g.sum((double)a0 + (double)a1, g.sh->sums[parity][0]) * p.inv_d;
   } else {
-    uint64_t acc[2] = {0, 0};
-    int n = 0;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      n += has(k) ? 8 : 0;
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i & 1] = add2(acc[i & 1], widen(word(v[k], i)));
-    }
-    float a0, a1;
+      for (int i = 0; i < 4; ++i) acc[i & 1] = add2(acc[i & 1], v(k, i));
     upk2(add2(acc[0], acc[1]), a0, a1);
-    const float S = a0 + a1, m = n ? S / (float)n : 0.0f;
+    const float n = full ? 8.0f * NV : 8.0f * (NV - 1);
+    const float S = a0 + a1, m = S * (full ? 1.0f / (8.0f * NV) : NV > 1 ? 1.0f / (8.0f * (NV - 1)) : 0.0f);
     acc[0] = acc[1] = 0;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (has(k)) {
+    for (int k = 0; k < NV; ++k) {
+      const float c = k < NV - 1 || full ? -m : 0.0f;  // zeros stay zeros
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint64_t d = add2(widen(word(v[k], i)), pk2(-m, -m));
-          acc[i & 1] = fma2(d, d, acc[i & 1]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t d = add2(v(k, i), pk2(c, c));
+        acc[i & 1] = fma2(d, d, acc[i & 1]);
       }
+    }
     upk2(add2(acc[0], acc[1]), a0, a1);
     double s1 = S, s2 = ((double)a0 + (double)a1) + (double)m * (2.0 * S - (double)n * m);
 #pragma unroll
@@ -192,11 +194,12 @@ norm_quant_rows(const QuantParams p) {
       s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
       s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
     }
-    if (!WARP_ROW) {
-      if ((tid & 31) == 0) sums[0][tid >> 5] = s1, sums[1][tid >> 5] = s2;
-      __syncthreads();
+    if (g.T > 32) {
+      double(&sums)[2][kMaxWarps] = g.sh->sums[parity];
+      if ((g.tid & 31) == 0) sums[0][g.tid >> 5] = s1, sums[1][g.tid >> 5] = s2;
+      g.meet();
       s1 = sums[0][0], s2 = sums[1][0];
-      for (int w = 1; w < (T >> 5); ++w) s1 += sums[0][w], s2 += sums[1][w];
+      for (int w = 1; w < (g.T >> 5); ++w) s1 += sums[0][w], s2 += sums[1][w];
     }
     mu = s1 * p.inv_d;
     var = s2 * p.inv_d - mu * mu;
@@ -205,22 +208,21 @@ norm_quant_rows(const QuantParams p) {
   // mean, zeros, infinities, NaN) take their statistics from fp64, around the exact mean.
   // The branch is the same for all threads of a row. The thread reads its vectors again (its
   // own r stores, or x) in rolled loops: walking the registers here would set the register
-  // allocation of the whole kernel (118-128 registers with spills, against 80).
+  // allocation of the whole kernel.
   if (!(var >= 0x1p-80 && var <= 0x1p+100 && mu * mu <= 1024.0 * var)) {
-    const uint4* again = reinterpret_cast<const uint4*>(p.res ? p.r + (b * p.r_sb + l * p.r_sl) : xr);
     double c = 0.0;
     if (!IS_RMS) {
 #pragma unroll 1
-      for (int j = tid; j < (int)p.vecs; j += T) {
+      for (int j = g.tid; j < (int)p.vecs; j += g.T) {
         const uint4 u = __ldcg(again + j);
 #pragma unroll
         for (int i = 0; i < 4; ++i) c += bf16_f64<0>(word(u, i)) + bf16_f64<1>(word(u, i));
       }
-      mu = row_sum<WARP_ROW>(c, sums[2]) * p.inv_d;
+      mu = g.sum(c, g.sh->again[0]) * p.inv_d;
       c = 0.0;
     }
 #pragma unroll 1
-    for (int j = tid; j < (int)p.vecs; j += T) {
+    for (int j = g.tid; j < (int)p.vecs; j += g.T) {
       const uint4 u = __ldcg(again + j);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -228,100 +230,200 @@ norm_quant_rows(const QuantParams p) {
         c = fma(d1, d1, fma(d0, d0, c));
       }
     }
-    var = row_sum<WARP_ROW>(c, sums[3]) * p.inv_d;
+    var = g.sum(c, g.sh->again[1]) * p.inv_d;
   }
-  const float rho = (float)rsqrt(var + p.eps);
-  const float mu_hi = (float)mu, mu_lo = (float)(mu - (double)mu_hi);  // r - mu keeps fp32's precision
+  const float hi = (float)mu;
+  return Stats{(float)rsqrt(var + p.eps), hi, (float)(mu - (double)hi)};
+}
 
-  // ---- y in fp32, and the row's largest magnitude ---------------------------------------
-  uint64_t y[NV][4];
-  uint32_t top = 0;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int j = tid + k * T;
-    if (!has(k)) continue;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint64_t d = widen(word(v[k], i));
-      if (!IS_RMS) d = add2(add2(d, pk2(-mu_hi, -mu_hi)), pk2(-mu_lo, -mu_lo));
-      y[k][i] = mul2(d, pk2(rho, rho));
-    }
-    if (p.weight) {
-      uint64_t w[4];
-      load_affine(p.weight, p.affine_fp32, j, w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[k][i] = mul2(y[k][i], w[i]);
-    }
-    if (p.bias) {
-      uint64_t w[4];
-      load_affine(p.bias, p.affine_fp32, j, w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[k][i] = add2(y[k][i], w[i]);
-    }
-    if (ROW_MOD || p.scale) {
-      const uint4 s = ROW_MOD ? sv[k] : __ldg(reinterpret_cast<const uint4*>(sr) + j);
-      const uint4 t = ROW_MOD ? tv[k] : __ldg(reinterpret_cast<const uint4*>(tr) + j);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        y[k][i] = fma2(y[k][i], add2(widen(word(s, i)), pk2(1.0f, 1.0f)), widen(word(t, i)));
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a0, a1;
-      upk2(y[k][i], a0, a1);
-      top = max(top, max(__float_as_uint(a0) & 0x7FFFFFFFu, __float_as_uint(a1) & 0x7FFFFFFFu));
-    }
-  }
-  const float a = __uint_as_float(row_max<WARP_ROW>(top, tops));
+// SHARED: the operands come from shared memory, rows one after another; otherwise one row per
+// group, with its operands (MOD: scale and shift are read with the row and wait in registers).
+// ADD: y = n a + b has a b.
+template <int NV, bool IS_RMS, bool SHARED, bool MOD, bool ADD>
+__global__ void __launch_bounds__(kMaxThreads, 1) norm_quant_rows(const __grid_constant__ QuantParams p) {
+  __shared__ GroupShared groups[kMaxWarps];
+  extern __shared__ __align__(16) uint4 kept[];  // SHARED: a and b in halves of a vector's eight, the gate
+  const Group g{&groups[threadIdx.y], (int)threadIdx.y, (int)threadIdx.x, (int)blockDim.x};
+  const int T = g.T, tid = g.tid;
+  const bool full = (uint32_t)(tid + (NV - 1) * T) < p.vecs;
+  auto has = [&](int k) { return k < NV - 1 || full; };
+  const uint32_t begin = blockIdx.x * p.chunk, end = min(begin + p.chunk, p.rows);
+  uint32_t row = begin + threadIdx.y;
 
-  // ---- scale and quantise ------------------------------------------------------------------
-  // The product with 448 / a stands for the quotient by row_scale: one rounding less than
-  // dividing by the rounded row_scale. fmaxf would drop a NaN, so the floor is a comparison.
-  const float a1 = a < 0x1p-100f ? 0x1p-100f : a;
-  if (tid == 0) p.row_scale[row] = a == 0.0f ? 1.0f : a1 / 448.0f;
-  const float inv = 448.0f / a1;
-  uint8_t* qo = p.q + (b * p.q_sb + l * p.q_sl);
+  uint4 xv[NV], rv[NV];
+  auto load = [&](const RowAt& at) {
+    const uint4* x = reinterpret_cast<const uint4*>(at_row(p.x, p.x_sb, p.x_sf, p.x_sl, at)) + tid;
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    if (!has(k)) continue;
-    uint32_t h[4];
+    for (int k = 0; k < NV; ++k, x += T)
+      if (has(k)) xv[k] = p.stream_mask & kX ? __ldcs(x) : *x;
+    if (p.res) {
+      const uint4* r = reinterpret_cast<const uint4*>(at_row(p.res, p.res_sb, p.res_sf, p.res_sl, at)) + tid;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float2 e;
-      upk2(mul2(y[k][i], pk2(inv, inv)), e.x, e.y);
-      h[i] = __nv_cvt_float2_to_fp8x2(e, __NV_SATFINITE, __NV_E4M3);
+      for (int k = 0; k < NV; ++k, r += T)
+        if (has(k)) rv[k] = p.stream_mask & kRes ? __ldcs(r) : *r;
     }
-    __stcs(reinterpret_cast<uint2*>(qo) + tid + k * T, make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16));
+  };
+#pragma unroll
+  for (int k = 0; k < NV; ++k) xv[k] = rv[k] = make_uint4(0, 0, 0, 0);
+  RowAt at = row_at(p, row);
+  if (row < end) load(at);
+
+  int parity = 0;
+  for (uint32_t seg = SHARED ? div_u32(begin, p.div_segment) : 0u;; ++seg) {
+    const uint32_t seg_end = SHARED ? (uint32_t)min((uint64_t)end, (uint64_t)(seg + 1) * p.segment) : end;
+    if (SHARED) {
+      // The operands of the rows up to seg_end; NV T vectors, zeros past the row's end.
+      const RowAt first = row_at(p, min(seg * p.segment, p.rows - 1));
+      const uint4* sr = reinterpret_cast<const uint4*>(at_row(p.scale, p.scale_sb, p.scale_sf, 0, first));
+      const uint4* tr = reinterpret_cast<const uint4*>(at_row(p.shift, p.shift_sb, p.shift_sf, 0, first));
+      const uint4* gr = reinterpret_cast<const uint4*>(at_row(p.gate, p.gate_sb, p.gate_sf, 0, first));
+      __syncthreads();
+      const int all = NV * T;
+      for (int j = threadIdx.y * T + tid; j < all; j += T * blockDim.y) {
+        uint64_t a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+        uint4 gate = make_uint4(0, 0, 0, 0);
+        if ((uint32_t)j < p.vecs) {
+          uint4 s = gate, t = gate;
+          if (p.scale) s = __ldg(sr + j), t = __ldg(tr + j);
+          coefficients(p, j, p.scale != nullptr, s, t, a, b);
+          if (p.gate) gate = __ldg(gr + j);
+        }
+        ulonglong2* to = reinterpret_cast<ulonglong2*>(kept);
+        to[j] = make_ulonglong2(a[0], a[1]), to[j + all] = make_ulonglong2(a[2], a[3]);
+        if (p.gate) kept[j + 2 * all] = gate;
+        if (ADD) to[j + 3 * all] = make_ulonglong2(b[0], b[1]), to[j + 4 * all] = make_ulonglong2(b[2], b[3]);
+      }
+      __syncthreads();
+    }
+    for (; row < seg_end; row += blockDim.y, parity ^= 1) {
+      // ---- r = residual + gate x, or x ----------------------------------------------------
+      uint64_t y[NV][4];
+      const uint4* again = reinterpret_cast<const uint4*>(at_row(p.x, p.x_sb, p.x_sf, p.x_sl, at));
+      if (p.res) {
+        if (p.gate) {
+          const uint4* gr = SHARED ? kept + 2 * NV * T : reinterpret_cast<const uint4*>(at_row(p.gate, p.gate_sb, p.gate_sf, p.gate_sl, at));
+          gr += tid;
+#pragma unroll
+          for (int k = 0; k < NV; ++k, gr += T)
+            if (SHARED || has(k)) xv[k] = residual_vec<true>(rv[k], xv[k], SHARED ? *gr : p.stream_mask & kGate ? __ldcs(gr) : __ldg(gr));
+        } else {
+#pragma unroll
+          for (int k = 0; k < NV; ++k) xv[k] = residual_vec<false>(rv[k], xv[k], xv[k]);
+        }
+        uint4* ro = reinterpret_cast<uint4*>(p.r + (at.b * p.r_sb + at.l * p.r_sl));
+        again = ro;
+        ro += tid;
+#pragma unroll
+        for (int k = 0; k < NV; ++k, ro += T)
+          if (has(k)) __stcs(ro, xv[k]);
+      }
+      // Its values in fp32: kept where the next row's vectors take their place, otherwise widened
+      // when they are used (modulation waits in registers meanwhile).
+      if (SHARED) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[k][i] = widen(has(k) ? word(xv[k], i) : 0u);
+      }
+      auto value = [&](int k, int i) { return SHARED ? y[k][i] : widen(word(xv[k], i)); };
+
+      uint4 sv[MOD ? NV : 1], tv[MOD ? NV : 1];
+      if (MOD) {  // the statistics hide its latency
+        const uint4* sr = reinterpret_cast<const uint4*>(at_row(p.scale, p.scale_sb, p.scale_sf, p.scale_sl, at)) + tid;
+        const uint4* tr = reinterpret_cast<const uint4*>(at_row(p.shift, p.shift_sb, p.shift_sf, p.shift_sl, at)) + tid;
+#pragma unroll
+        for (int k = 0; k < NV; ++k, sr += T, tr += T)
+          if (has(k)) {
+            sv[k] = p.stream_mask & kScale ? __ldcs(sr) : __ldg(sr);
+            tv[k] = p.stream_mask & kShift ? __ldcs(tr) : __ldg(tr);
+          }
+      }
+      const RowAt next = row_at(p, row + blockDim.y);
+      if (SHARED && row + blockDim.y < end) load(next);
+
+      const Stats st = statistics<NV, IS_RMS>(p, g, parity, value, full, again);
+
+      if (!SHARED) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) xv[k] = here(xv[k]);
+      }
+
+      // ---- y in fp32, and the row's largest magnitude -------------------------------------
+      float top = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        uint64_t a[4], b[4];
+        if (SHARED) {
+          const ulonglong2* from = reinterpret_cast<const ulonglong2*>(kept) + (tid + k * T);
+          const ulonglong2 a0 = from[0], a1 = from[NV * T];
+          a[0] = a0.x, a[1] = a0.y, a[2] = a1.x, a[3] = a1.y;
+          if (ADD) {
+            const ulonglong2 b0 = from[3 * NV * T], b1 = from[4 * NV * T];
+            b[0] = b0.x, b[1] = b0.y, b[2] = b1.x, b[3] = b1.y;
+          }
+        } else if (has(k)) {
+          coefficients(p, tid + k * T, MOD, sv[MOD ? k : 0], tv[MOD ? k : 0], a, b);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = b[i] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint64_t d = value(k, i);
+          if (!IS_RMS) d = add2(add2(d, pk2(-st.mu_hi, -st.mu_hi)), pk2(-st.mu_lo, -st.mu_lo));
+          d = mul2(d, pk2(st.rho, st.rho));
+          y[k][i] = ADD ? fma2(d, a[i], b[i]) : mul2(d, a[i]);
+          float a0, a1;
+          upk2(y[k][i], a0, a1);
+          top = max_abs(top, a0, a1);
+        }
+      }
+      const float a = g.max(top, g.sh->tops[parity]);
+
+      // ---- scale and quantise --------------------------------------------------------------
+      // The product with 448 / a stands for the quotient by row_scale: one rounding less than
+      // dividing by the rounded row_scale. fmaxf would drop a NaN, so the floor is a comparison.
+      const float a1 = a < 0x1p-100f ? 0x1p-100f : a;
+      if (tid == 0) p.row_scale[row] = a == 0.0f ? 1.0f : a1 / 448.0f;
+      const float inv = 448.0f / a1;
+      uint2* qo = reinterpret_cast<uint2*>(p.q + (at.b * p.q_sb + at.l * p.q_sl)) + tid;
+#pragma unroll
+      for (int k = 0; k < NV; ++k, qo += T) {
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2 e;
+          upk2(mul2(y[k][i], pk2(inv, inv)), e.x, e.y);
+          h[i] = __nv_cvt_float2_to_fp8x2(e, __NV_SATFINITE, __NV_E4M3);
+        }
+        if (has(k)) __stcs(qo, make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16));
+      }
+      at = next;
+    }
+    if (seg_end >= end) return;
   }
 }
 
+// As few threads as five vectors each allow.
 struct Shape {
   int nv, threads;
-  bool warp_row;
 };
-
-// One warp per row up to 1024 channels; beyond, four or five vectors per thread, whichever
-// leaves fewer lanes without a vector (five where both fit).
 Shape shape_of(int D) {
-  const int V = D / 8;
-  if (V <= 128) return Shape{(V + 31) / 32, 32, true};
-  const int t4 = (V + 127) / 128 * 32, t5 = (V + 159) / 160 * 32;
-  return t5 * 5 <= t4 * 4 ? Shape{5, t5, false} : Shape{4, t4, false};
+  const int V = D / 8, T = (V + 32 * kMaxVectors - 1) / (32 * kMaxVectors) * 32;
+  return Shape{(V + T - 1) / T, T};
 }
 
 using Kernel = void (*)(QuantParams);
 
-template <bool RMS, bool MOD>
-Kernel pick(const Shape& s) {
-  if (s.warp_row) {
-    switch (s.nv) {
-      case 1: return norm_quant_rows<1, RMS, MOD, true>;
-      case 2: return norm_quant_rows<2, RMS, MOD, true>;
-      case 3: return norm_quant_rows<3, RMS, MOD, true>;
-      default: return norm_quant_rows<4, RMS, MOD, true>;
-    }
+template <bool RMS, bool SHARED, bool MOD, bool ADD>
+Kernel pick(int nv) {
+  switch (nv) {
+    case 1: return norm_quant_rows<1, RMS, SHARED, MOD, ADD>;
+    case 2: return norm_quant_rows<2, RMS, SHARED, MOD, ADD>;
+    case 3: return norm_quant_rows<3, RMS, SHARED, MOD, ADD>;
+    case 4: return norm_quant_rows<4, RMS, SHARED, MOD, ADD>;
+    default: return norm_quant_rows<5, RMS, SHARED, MOD, ADD>;
   }
-  return s.nv == 4 ? norm_quant_rows<4, RMS, MOD, false> : norm_quant_rows<5, RMS, MOD, false>;
 }
 
 }  // namespace
@@ -332,7 +434,8 @@ using namespace block_ops;
 struct norm_quant_s {
   nq_config cfg;
   Shape shape;
-  Kernel kernel, kernel_row_mod;
+  Kernel each, each_mod, shared;  // a row per group, the same with modulation, persistent
+  size_t kept;                    // bytes of shared memory of the last
 };
 
 namespace {
@@ -430,8 +533,16 @@ fn_status norm_quant_create(norm_quant_t* out, const nq_config* cfg) {
   if (!h) return FN_ERR_INVALID_ARG;
   h->cfg = c;
   h->shape = shape_of(c.D);
-  h->kernel = c.is_rms ? pick<true, false>(h->shape) : pick<false, false>(h->shape);
-  h->kernel_row_mod = c.is_rms ? pick<true, true>(h->shape) : pick<false, true>(h->shape);
+  const int nv = h->shape.nv;
+  const bool add = c.has_bias || c.has_modulation;
+  if (c.is_rms) {
+    h->each = pick<true, false, false, true>(nv), h->each_mod = pick<true, false, true, true>(nv);
+    h->shared = add ? pick<true, true, false, true>(nv) : pick<true, true, false, false>(nv);
+  } else {
+    h->each = pick<false, false, false, true>(nv), h->each_mod = pick<false, false, true, true>(nv);
+    h->shared = add ? pick<false, true, false, true>(nv) : pick<false, true, false, false>(nv);
+  }
+  h->kept = (size_t)nv * h->shape.threads * 16 * (add ? 5 : 3);
   *out = h;
   return FN_OK;
 }
@@ -441,13 +552,40 @@ fn_status norm_quant_validate(norm_quant_t h, const nq_args* a) { return validat
 fn_status norm_quant_launch(norm_quant_t h, const nq_args* a, fn_stream_t stream) {
   const fn_status s = validate(h, a);
   if (s != FN_OK || a->B == 0 || a->L == 0) return s;
-  const QuantParams p = make_params(h, a);
-  const bool row_mod = a->scale.stride_l != 0 || a->shift.stride_l != 0;
+  QuantParams p = make_params(h, a);
+  int device = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+  if (e != cudaSuccess) return launch_status(e);
+
+  // Rows that share gate, scale and shift, and the rows of a CTA.
+  const fn_operand* by_row[3] = {&a->gate, &a->scale, &a->shift};
+  bool own = false, by_batch = false, by_frame = false;
+  for (const fn_operand* o : by_row) own |= o->stride_l != 0, by_batch |= o->stride_b != 0, by_frame |= o->stride_f != 0;
+  p.segment = by_frame ? p.tpf : by_batch ? p.L : p.rows;
+  const int T = h->shape.threads, groups = kMaxThreads / T;
+  // The persistent kernel is ahead once every group has a row (D = 5120: 1184 rows 9.3 against
+  // 12.8 us, 9472 rows 62 against 94; below that a CTA to a row spreads wider) and an operand
+  // serves a row of each group (frames of 16 rows 67 against 100 us, of 2 164 against 112).
+  const bool shared = !own && p.rows >= (uint32_t)(sms * groups) && p.segment >= (uint32_t)(groups > 4 ? groups : 4);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(h->shape.warp_row ? (p.rows + kRowsPerCta - 1) / kRowsPerCta : p.rows);
-  cfg.blockDim = dim3(h->shape.threads, h->shape.warp_row ? kRowsPerCta : 1);
+  Kernel kernel;
+  if (shared) {
+    kernel = h->shared;
+    p.chunk = (p.rows + sms - 1) / sms;
+    p.div_segment = make_div_u32(p.segment);
+    cfg.blockDim = dim3(T, groups);
+    cfg.dynamicSmemBytes = h->kept;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)h->kept);
+    if (e != cudaSuccess) return launch_status(e);
+  } else {
+    kernel = p.scale ? h->each_mod : h->each;
+    p.chunk = T > 32 ? 1 : 8;
+    cfg.blockDim = dim3(T, p.chunk);
+  }
+  cfg.gridDim = dim3((p.rows + p.chunk - 1) / p.chunk);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  return launch_status(cudaLaunchKernelEx(&cfg, row_mod ? h->kernel_row_mod : h->kernel, p));
+  return launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
 fn_status norm_quant_destroy(norm_quant_t h) {

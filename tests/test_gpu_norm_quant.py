@@ -135,6 +135,46 @@ def test_rows_against_the_formula(case):
     check(*call(t, case[4]), **t, norm=case[4], eps=1e-6)
 
 
+# Many rows that share their operands: a row for every width of a thread's part, segments that
+# end inside a CTA's rows, rows that do not divide evenly.
+MANY = [
+    (1, 21000, 5120, 21, "layer", True, "frame", "frame", True, False, BF),
+    (3, 7001, 2320, 0, "layer", False, "none", "batch", True, True, torch.float32),
+    (1, 5003, 5136, 0, "rms", True, "bcast", "none", True, False, BF),
+    (2, 2600, 16368, 0, "rms", True, "batch", "bcast", False, True, BF),
+    (1, 2500, 10240, 2, "layer", True, "none", "frame", False, False, BF),
+    (1, 40001, 256, 0, "layer", True, "vec", "vec", True, True, BF),
+    (4, 12000, 512, 3, "rms", False, "none", "frame", False, False, BF),
+    (1, 30011, 752, 0, "layer", False, "none", "none", False, False, BF),
+    (1, 20011, 1008, 0, "rms", True, "bcast", "bcast", True, False, torch.float32),
+    (1, 19003, 1296, 0, "rms", True, "none", "none", False, True, BF),
+    (1, 6001, 3856, 0, "layer", True, "bcast", "bcast", True, True, torch.float32),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(str(v).replace("torch.", "") for v in c))
+def test_many_rows(case):
+    B, L, D, F, norm = case[:5]
+    t = make(case, 200)
+    q, s, r = call(t, norm)
+    for at in {0, L - 300, max(0, L // max(F, 1) - 150)}:  # rows around the first operands' change too
+        rows = slice(at, at + 300)
+        part = {k: per_token(v, B, L)[:, rows].to(BF) if k in ("gate", "scale", "shift") and v is not None
+                else v[:, rows] if k in ("x", "residual") and v is not None else v for k, v in t.items()}
+        check(q[:, rows], s[:, rows], r[:, rows] if r is not None else None, **part, norm=norm, eps=1e-6)
+        q2, s2, r2 = call(part, norm)  # few rows, with operands of their own: the same bits
+        assert torch.equal(q2.view(torch.uint8), q[:, rows].view(torch.uint8)) and torch.equal(s2, s[:, rows])
+        assert r is None or torch.equal(r2, r[:, rows])
+    # in place, and a row that fp32 sums do not serve among the others
+    if t["residual"] is not None:
+        t["x"][0, 5] = 0.0
+        t["residual"][0, 5] = 0.0
+        t["residual"][0, 6] *= 1e25
+        q, s, r = call(t, norm)
+        q2, s2, r2 = call(t, norm, residual_out=t["residual"])
+        assert torch.equal(q2.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s2, s) and torch.equal(r2, r)
+
+
 @pytest.mark.parametrize("D", [128, 5120])
 @pytest.mark.parametrize("norm", ["layer", "rms"])
 def test_rows_that_fp32_sums_do_not_serve(norm, D):
