@@ -1,8 +1,8 @@
 // Host side of linear_gate: checks, the choice of a kernel, tensor maps, launches.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstring>
-#include <cstdlib>
 #include <new>
 
 #include "host_checks.h"
@@ -126,16 +126,43 @@ fn_status launch_tokens(const linear_gate_s* h, LinearParams& p, cudaStream_t st
 // ---- many rows --------------------------------------------------------------------------------
 
 struct Variant {
-  int cg, bn, shared;
+  int cg, mh, bn, shared, stages, threads, received[9];  // received: bytes of sums by the parts of K, of a split tile
   void* kernel[3];  // by dtype: bf16, fp16, e4m3
+  int rows() const { return kTileM * cg * mh; }
 };
-template <int CG, int BN>
+template <int CG, int MH, int BN>
 Variant variant() {
-  return Variant{CG, BN, MatrixShape<CG, BN>::kShared,
-                 {(void*)linear_gate_tiles<CG, BN, false, false>, (void*)linear_gate_tiles<CG, BN, false, true>,
-                  (void*)linear_gate_tiles<CG, BN, true, false>}};
+  return Variant{CG, MH, BN, MatrixShape<CG, MH, BN>::kShared, MatrixShape<CG, MH, BN>::kStages, MatrixShape<CG, MH, BN>::kThreads, {},
+                 {(void*)linear_gate_tiles<CG, MH, BN, false, false>, (void*)linear_gate_tiles<CG, MH, BN, false, true>,
+                  MH == 2 ? nullptr : (void*)linear_gate_tiles<CG, 1, BN, true, false>}};
 }
-const Variant kVariants[] = {variant<2, 256>(), variant<1, 256>(), variant<1, 128>(), variant<1, 64>()};
+const Variant kVariants[] = {variant<2, 2, 256>(), variant<2, 1, 256>(), variant<1, 1, 256>(), variant<1, 1, 128>(), variant<1, 1, 64>()};
+
+template <int CG, int BN>
+Variant split_variant() {
+  using S = SplitShape<CG, BN>;
+  Variant v{CG, 1, BN, S::kShared, S::kStages, S::kThreads, {},
+            {(void*)linear_gate_split<CG, BN, false, false>, (void*)linear_gate_split<CG, BN, false, true>,
+             (void*)linear_gate_split<CG, BN, true, false>}};
+  for (int n = 1; n <= 8; ++n) v.received[n] = S::received(n);
+  return v;
+}
+const Variant kSplitVariants[] = {split_variant<2, 256>(), split_variant<1, 128>(), split_variant<1, 64>()};
+
+// Cycles of a step of K: the products, or the operands' way into an SM: 80 bytes a cycle, and
+// less where rows of 128 bytes start between lines (999 x 2048 x 1288 12.2 us, K = 2080 13.5,
+// 2064 14.9, 2056 19.1); and no step is shorter than its share of a load's 2500 cycles (16 x 5120
+// x 5120 as 80 CTAs of 8 stages: 335 cycles a step).
+int64_t step_cycles(const Variant& v, int64_t rows, int64_t row_bytes) {
+  const int64_t products = 2 * v.mh * v.bn;
+  const int64_t x = rows < kTileM * v.mh ? rows : kTileM * v.mh;  // rows past the last are not read
+  const int percent = row_bytes % 128 == 0 ? 100 : row_bytes % 64 == 0 ? 120 : row_bytes % 32 == 0 ? 140 : 200;
+  const int64_t bytes = (x + v.bn / v.cg) * kStepBytes * percent / 8000;
+  const int64_t least = 2500 / v.stages, most = products > bytes ? products : bytes;
+  return most > least ? most : least;
+}
+// What a tile takes besides: its way through the epilogue, which the next tile hides or not.
+int64_t drain_cycles(const Variant& v) { return 1500 + v.bn * v.mh * 16; }
 
 // A matrix of `rows` rows of `width` elements per batch, as a tensor map of boxes.
 struct Matrix {
@@ -166,6 +193,25 @@ fn_status encode(CUtensorMap* m, int dtype, const Matrix& a, int box_width, int 
   return r == CUDA_SUCCESS ? FN_OK : launch_status(cudaErrorInvalidValue);
 }
 
+// How many clusters of n parts of K run at once; asked once per variant (devices of one kind).
+fn_status clusters_at_once(const Variant& v, int n, int dtype, int* count) {
+  static std::atomic<int> known[3][9][3];
+  std::atomic<int>& k = known[&v - kSplitVariants][n][dtype];
+  *count = k.load(std::memory_order_relaxed);
+  if (*count) return FN_OK;
+  cudaError_t e = cudaFuncSetAttribute(v.kernel[dtype], cudaFuncAttributeMaxDynamicSharedMemorySize, v.shared);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n * v.cg), cfg.blockDim = dim3(v.threads), cfg.dynamicSmemBytes = v.shared;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = n * v.cg, cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
+  cfg.attrs = &cluster, cfg.numAttrs = 1;
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(count, v.kernel[dtype], &cfg);
+  if (e != cudaSuccess) return launch_status(e);
+  k.store(*count, std::memory_order_relaxed);
+  return FN_OK;
+}
+
 fn_status launch_tiles(const linear_gate_s* h, const lg_args* a, LinearParams& p, cudaStream_t stream) {
   const lg_config& c = h->cfg;
   int device = 0, sms = 0;
@@ -183,40 +229,60 @@ fn_status launch_tiles(const linear_gate_s* h, const lg_args* a, LinearParams& p
     return Matrix{ptr, width, rows, a->L == 1 ? sb : sl, batches, sb};
   };
 
+  const int64_t steps = (c.K * element_size(c) + kStepBytes - 1) / kStepBytes;
+  const int64_t row_bytes = (a->L > 1 ? a->x.stride_l : a->x.stride_b) * element_size(c) | a->weight_stride * element_size(c);
   const Variant* best = nullptr;
-  int64_t best_cost = 0;
+  int64_t best_cost = 0, parts = 1;
   for (const Variant& v : kVariants) {
-    const int64_t tm = (rows + kTileM * v.cg - 1) / (kTileM * v.cg) * batches, tn = (c.N + v.bn - 1) / v.bn;
+    // The sums of a 512-row tile fill TMEM, so its epilogue costs some 7000 cycles that two tiles
+    // in turn hide. Over 80 steps of 16-bit operands the power saved is worth more (176400 x 5120 x
+    // 5120 sustained: 7.94 against 8.27 ms); over 40 steps of e4m3 it is not (4.43 against 3.98 ms).
+    if (v.mh == 2 && (c.dtype == BO_E4M3 || steps < 64)) continue;
+    const int64_t tm = (rows + v.rows() - 1) / v.rows() * batches, tn = (c.N + v.bn - 1) / v.bn;
     const int64_t waves = (tm * tn + sms / v.cg - 1) / (sms / v.cg);
-    // a tile's time: its products, and what does not shrink with it
-    const int64_t cost = waves * (v.bn + (v.cg == 2 ? 0 : 32));
+    int64_t cost = waves * steps * step_cycles(v, rows, row_bytes);
+    if (v.mh == 2) cost -= cost / 32;
+    cost += drain_cycles(v);
     if (!best || cost < best_cost) best = &v, best_cost = cost;
   }
-  if (getenv("LG_VARIANT")) best = &kVariants[atoi(getenv("LG_VARIANT"))];
+  // Few tiles: K split over a cluster, where its CTAs all run at once. Exchanging the sums takes
+  // some 8500 cycles for 128 columns, 13000 for 256.
+  for (const Variant& v : kSplitVariants) {
+    const int64_t tiles = (rows + v.rows() - 1) / v.rows() * batches * ((c.N + v.bn - 1) / v.bn);
+    for (int n = 2; n * v.cg <= 8 && n * 2 <= steps; ++n) {
+      if (tiles * n * v.cg > sms || v.received[n] > v.shared - 1024) continue;
+      const int64_t cost = (steps + n - 1) / n * step_cycles(v, rows, row_bytes) + 4000 + 35 * v.bn + drain_cycles(v) / n;
+      if (cost >= best_cost) continue;
+      int resident = 0;
+      const fn_status s = clusters_at_once(v, n, c.dtype, &resident);
+      if (s != FN_OK) return s;
+      if (tiles <= resident) best = &v, best_cost = cost, parts = n;
+    }
+  }
   const Variant& v = *best;
   const int size = element_size(c);
   p.batch_rows = (uint32_t)rows, p.batches = (uint32_t)batches;
-  p.tiles_m = (uint32_t)((rows + kTileM * v.cg - 1) / (kTileM * v.cg)), p.tiles_n = (uint32_t)((c.N + v.bn - 1) / v.bn);
+  p.tiles_m = (uint32_t)((rows + v.rows() - 1) / v.rows()), p.tiles_n = (uint32_t)((c.N + v.bn - 1) / v.bn);
   const int64_t tiles = (int64_t)p.tiles_m * p.batches * p.tiles_n;
   if (tiles > kMaxRows) return FN_ERR_INVALID_ARG;
   p.tiles = (uint32_t)tiles;
-  p.group = getenv("LG_GROUP") ? atoi(getenv("LG_GROUP")) : 8;
+  p.group = 8;
   p.div_band = fused_norm_impl::make_div_u32(p.group * p.tiles_n);
   p.div_tiles_m = fused_norm_impl::make_div_u32(p.tiles_m);
-  p.steps = (uint32_t)((c.K * size + kStepBytes - 1) / kStepBytes);
+  p.steps = (uint32_t)steps;
   // fp32 sums (bit 4), operand types (fp16 0, bf16 1; e4m3 0), N / 8 at bit 17, M / 16 at bit 24
   const uint32_t type = c.dtype == BO_BF16 ? 1u : 0u;
   p.idesc = 1u << 4 | type << 7 | type << 10 | (uint32_t)(v.bn / 8) << 17 | (uint32_t)(kTileM * v.cg / 16) << 24;
 
   const int out_type = c.dtype == BO_FP16 ? BO_FP16 : BO_BF16, per_step = kStepBytes / size;
-  CUtensorMap mx, mw, mo, mr;
-  fn_status s = encode(&mx, c.dtype, matrix(a->x.ptr, c.K, a->x.stride_b, a->x.stride_l), per_step, kTileM, CU_TENSOR_MAP_SWIZZLE_128B);
+  CUtensorMap mx, mw, mo = {}, mr;
+  fn_status s = encode(&mx, c.dtype, matrix(a->x.ptr, c.K, a->x.stride_b, a->x.stride_l), per_step, kTileM * v.mh, CU_TENSOR_MAP_SWIZZLE_128B);
   if (s == FN_OK)
     s = encode(&mw, c.dtype, Matrix{a->weight, c.K, c.N, a->weight_stride, 1, 0}, per_step, v.bn / v.cg, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (s == FN_OK)
+  if (s == FN_OK && parts == 1)
     s = encode(&mo, out_type, matrix(a->out, c.N, a->out_stride_b, a->out_stride_l), kBox, kBox, CU_TENSOR_MAP_SWIZZLE_64B);
   mr = mo;
-  if (s == FN_OK && c.has_residual)
+  if (s == FN_OK && parts == 1 && c.has_residual)
     s = encode(&mr, out_type, matrix(a->residual.ptr, c.N, a->residual.stride_b, a->residual.stride_l), kBox, kBox,
                CU_TENSOR_MAP_SWIZZLE_64B);
   if (s != FN_OK) return s;
@@ -224,18 +290,18 @@ fn_status launch_tiles(const linear_gate_s* h, const lg_args* a, LinearParams& p
   void* kernel = v.kernel[c.dtype];
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.shared);
   if (e != cudaSuccess) return launch_status(e);
-  const int64_t resident = sms / v.cg;
+  const int64_t resident = sms / v.cg;  // a split tile's CTAs are not persistent
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((tiles < resident ? tiles : resident) * v.cg));
-  cfg.blockDim = dim3(kMatrixThreads);
+  cfg.gridDim = dim3((unsigned)((tiles < resident || parts > 1 ? tiles : resident) * v.cg * parts));
+  cfg.blockDim = dim3(v.threads);
   cfg.dynamicSmemBytes = v.shared;
   cfg.stream = stream;
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = v.cg, cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
+  cluster.val.clusterDim.x = v.cg * parts, cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
   cfg.attrs = &cluster;
-  cfg.numAttrs = v.cg > 1 ? 1 : 0;
-  void* args[] = {&p, &mx, &mw, &mo, &mr};
+  cfg.numAttrs = v.cg * parts > 1 ? 1 : 0;
+  void* args[] = {&p, &mx, &mw, &mo, &mr};  // the first three where K is split
   return launch_status(cudaLaunchKernelExC(&cfg, kernel, args));
 }
 

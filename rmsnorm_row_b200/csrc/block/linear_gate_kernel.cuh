@@ -6,11 +6,14 @@
 //
 // Many rows: persistent CTAs or CTA pairs (CG = 2) of ten warps. One thread loads 128-byte
 // wide tiles of x and W by TMA into a ring of shared-memory stages, one thread issues the
-// tcgen05 products of a 128 CG x BN tile into TMEM, eight warps read the sums back, a row per
-// thread, and finish them. TMEM holds two tiles, so the epilogue of one runs under the
-// products of the next. A pair shares W's tile: each CTA loads half of it. Residual and output
-// pass through shared memory in boxes of 32 x 32: TMA brings a warp's next residual box while
-// the present one is worked on in place, and stores it.
+// tcgen05 products of a 128 MH CG x BN tile into TMEM, eight warps read the sums back, a row per
+// thread, and finish them. A pair shares W's tile: each CTA loads half of it. TMEM holds two
+// blocks of sums, so that the epilogue of one runs under the products of the other: two tiles in
+// turn (MH = 1), or two blocks of rows of one tile (MH = 2), which read W once. Large problems
+// are bound by the power that the chip may draw, and the operands' way from L2 takes its share:
+// a 512 x 256 tile moves a quarter less than a 256 x 256 one. Residual and output pass through
+// shared memory in boxes of 32 x 32: TMA brings a warp's next residual box while the present
+// one is worked on in place, and stores it.
 //
 // A few tokens: every warp streams rows of W past the tokens with 16-byte loads.
 #pragma once
@@ -169,19 +172,22 @@ constexpr int kTileM = 128;          // rows of a CTA
 constexpr int kStepBytes = 128;      // of K, per row and stage
 constexpr int kMaxStages = 8;
 constexpr int kEpilogueWarps = 8;    // two to each quarter of the rows, each half of the columns
-constexpr int kMatrixThreads = 32 * (2 + kEpilogueWarps);
 constexpr int kBox = 32;             // rows and columns of an output box
 constexpr int kBoxBytes = kBox * kBox * 2;
-constexpr int kBoxes = 4;            // of a warp: two being brought, one worked on, one being stored
-constexpr int kBoxesBytes = kEpilogueWarps * kBoxes * kBoxBytes;
 
-template <int CG, int BN>
+// CG CTAs work on a tile together, each on MH blocks of kTileM rows and all BN columns of it.
+template <int CG, int MH, int BN>
 struct MatrixShape {
-  static constexpr int kABytes = kTileM * kStepBytes, kBBytes = BN / CG * kStepBytes;
+  static constexpr int kABytes = MH * kTileM * kStepBytes, kBBytes = BN / CG * kStepBytes;
   static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kBoxes = MH == 2 ? 2 : 4;  // of a warp: half of them being brought, one worked on, the rest being stored
+  static constexpr int kBoxesBytes = kEpilogueWarps * kBoxes * kBoxBytes;
   static constexpr int kFit = (226 * 1024 - 1024 - kBoxesBytes) / kStageBytes;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-  static constexpr int kColumns = 2 * BN;  // TMEM: two tiles of sums
+  // Loading, products, then the epilogue's warps. With MH = 2 these are warpgroups of their own,
+  // which take over registers of the first: 40 + 2 x 232 of the 3 x 168 at launch.
+  static constexpr int kFirst = MH == 2 ? 4 : 2, kThreads = 32 * (kFirst + kEpilogueWarps);
+  static constexpr int kColumns = 2 * BN;  // TMEM: two blocks of sums
   static constexpr int kShared = kStages * kStageBytes + kBoxesBytes + 1024;  // 1024: alignment
 };
 
@@ -201,12 +207,13 @@ __device__ __forceinline__ Tile tile_at(const LinearParams& p, uint32_t t) {
 
 __device__ int linear_gate_gave_up = 0;  // launches in which a wait ran out (this file is included once)
 
-template <int CG, int BN, bool FP8, bool FP16>
-__global__ void __launch_bounds__(kMatrixThreads, 1)
+template <int CG, int MH, int BN, bool FP8, bool FP16>
+__global__ void __launch_bounds__(MatrixShape<CG, MH, BN>::kThreads, 1)
 linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant__ CUtensorMap map_x,
                   const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_out,
                   const __grid_constant__ CUtensorMap map_residual) {
-  using S = MatrixShape<CG, BN>;
+  using S = MatrixShape<CG, MH, BN>;
+  constexpr int kBoxes = S::kBoxes, kAhead = kBoxes / 2;
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], sums_full[2], sums_empty[2];
   __shared__ __align__(8) uint64_t box_full[kEpilogueWarps][kBoxes];
@@ -223,6 +230,12 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
     failed = 0;
     mbar_init_fence();
   }
+  if (threadIdx.x == 64) {
+    prefetch_map(&map_x);
+    prefetch_map(&map_w);
+    prefetch_map(&map_out);
+    if (p.has_residual) prefetch_map(&map_residual);
+  }
   if (warp == 1) tmem_alloc<CG>(smem_u32(&tmem_at), S::kColumns);
   __syncthreads();
   if (CG == 2) cluster_sync();
@@ -230,105 +243,161 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
   const uint32_t tmem = *(volatile uint32_t*)&tmem_at;
 
   const uint32_t first = blockIdx.x / CG, step = gridDim.x / CG;
-  if (warp == 0) {
-    if (elect_one()) {
-      prefetch_map(&map_x);
-      prefetch_map(&map_w);
-      constexpr int kElems = FP8 ? 128 : 64;  // of K, per step
-      uint32_t stage = 0, parity = 0;
-      bool ok = true;
-      for (uint32_t t = first; ok && t < p.tiles; t += step) {
-        const Tile at = tile_at(p, t);
-        const int row = (int)((at.m * CG + rank) * kTileM), col = (int)(at.n * BN + rank * (BN / CG));
-        for (uint32_t k = 0; k < p.steps; ++k) {
-          if (!(ok = mbar_wait(smem_u32(&empty[stage]), parity ^ 1, &failed))) break;
-          uint32_t bar = smem_u32(&full[stage]);
-          if (rank == 0) mbar_expect(bar, CG * S::kStageBytes);
-          if (CG == 2) bar = map_to(bar, 0);
-          const uint32_t a = stages + stage * S::kStageBytes;
-          tma_load<CG == 2>(a, &map_x, (int)k * kElems, row, (int)at.batch, bar);
-          tma_load<CG == 2>(a + S::kABytes, &map_w, (int)k * kElems, col, 0, bar);
+  if (warp < S::kFirst) {
+    if (MH == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) {
+      if (elect_one()) {
+        constexpr int kElems = FP8 ? 128 : 64;  // of K, per step
+        uint32_t stage = 0, parity = 0;
+        bool ok = true;
+        for (uint32_t t = first; ok && t < p.tiles; t += step) {
+          const Tile at = tile_at(p, t);
+          const int row = (int)((at.m * CG + rank) * MH * kTileM), col = (int)(at.n * BN + rank * (BN / CG));
+          for (uint32_t k = 0; k < p.steps; ++k) {
+            if (!(ok = mbar_wait(smem_u32(&empty[stage]), parity ^ 1, &failed))) break;
+            uint32_t bar = smem_u32(&full[stage]);
+            if (rank == 0) mbar_expect(bar, CG * S::kStageBytes);
+            if (CG == 2) bar = map_to(bar, 0);
+            const uint32_t a = stages + stage * S::kStageBytes;
+            tma_load<CG == 2>(a, &map_x, (int)k * kElems, row, (int)at.batch, bar);
+            tma_load<CG == 2>(a + S::kABytes, &map_w, (int)k * kElems, col, 0, bar);
+            if (++stage == S::kStages) stage = 0, parity ^= 1;
+          }
+        }
+        // The last copies have landed when their stages are free again.
+        for (int i = 0; ok && i < S::kStages; ++i) {
+          ok = mbar_wait(smem_u32(&empty[stage]), parity ^ 1, &failed);
           if (++stage == S::kStages) stage = 0, parity ^= 1;
         }
       }
-      // The last copies have landed when their stages are free again.
-      for (int i = 0; ok && i < S::kStages; ++i) {
-        ok = mbar_wait(smem_u32(&empty[stage]), parity ^ 1, &failed);
-        if (++stage == S::kStages) stage = 0, parity ^= 1;
-      }
-    }
-  } else if (warp == 1) {
-    if (rank == 0 && elect_one()) {
-      uint32_t stage = 0, parity = 0, n = 0;
-      bool ok = true;
-      for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
-        const uint32_t buf = n & 1, round = (n >> 1) & 1;
-        if (!(ok = mbar_wait(smem_u32(&sums_empty[buf]), round ^ 1, &failed))) break;
-        tc_fence_after();
-        for (uint32_t k = 0; k < p.steps; ++k) {
-          if (!(ok = mbar_wait(smem_u32(&full[stage]), parity, &failed))) break;
-          tc_fence_after();
-          const uint32_t a = stages + stage * S::kStageBytes;
-          const uint64_t da = operand_desc(a), db = operand_desc(a + S::kABytes);
+    } else if (warp == 1) {
+      if (rank == 0 && elect_one()) {
+        uint32_t stage = 0, parity = 0, n = 0;
+        bool ok = true;
+        // The products of block `half` with stage s into its sums.
+        auto multiply = [&](uint32_t s, uint32_t acc, int half, bool add) {
+          const uint32_t a = stages + s * S::kStageBytes;
+          const uint64_t da = operand_desc(a + half * kTileM * kStepBytes), db = operand_desc(a + S::kABytes);
 #pragma unroll
           for (int i = 0; i < kStepBytes / 32; ++i)  // 32 bytes of K each
-            mma<CG, FP8>(tmem + buf * BN, da + 2 * i, db + 2 * i, p.idesc, k > 0 || i > 0);
-          mma_commit<CG>(smem_u32(&empty[stage]));
-          if (++stage == S::kStages) stage = 0, parity ^= 1;
+            mma<CG, FP8>(tmem + acc * BN, da + 2 * i, db + 2 * i, p.idesc, add || i > 0);
+        };
+        auto wait_full = [&](uint32_t s, uint32_t par) {
+          const bool got = mbar_wait(smem_u32(&full[s]), par, &failed);
+          tc_fence_after();
+          return got;
+        };
+        if (MH == 1) {
+          for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
+            const uint32_t buf = n & 1, round = (n >> 1) & 1;
+            if (!(ok = mbar_wait(smem_u32(&sums_empty[buf]), round ^ 1, &failed))) break;
+            tc_fence_after();
+            for (uint32_t k = 0; k < p.steps; ++k) {
+              if (!(ok = wait_full(stage, parity))) break;
+              multiply(stage, buf, 0, k > 0);
+              mma_commit<CG>(smem_u32(&empty[stage]));
+              if (++stage == S::kStages) stage = 0, parity ^= 1;
+            }
+            if (ok) mma_commit<CG>(smem_u32(&sums_full[buf]));
+          }
+        } else {
+          // Runs of stages, first block 0 and then block 1: long ones at a tile's ends, so that the
+          // sums of one block are read out while the other's products run; a stage elsewhere.
+          const uint32_t most = S::kStages - 1, ends = p.steps / 2 < most ? p.steps / 2 : most;
+          for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
+            for (uint32_t k = 0, run; ok && k < p.steps; k += run) {
+              run = (k == 0 || k + ends == p.steps) && ends > 1 ? ends : 1;
+              const bool last = k + run == p.steps;
+              uint32_t s = stage, par = parity;
+              if (k == 0) ok = mbar_wait(smem_u32(&sums_empty[0]), (n & 1) ^ 1, &failed);
+              for (uint32_t i = 0; ok && i < run; ++i) {
+                if (!(ok = wait_full(s, par))) break;
+                multiply(s, 0, 0, k + i > 0);
+                if (++s == S::kStages) s = 0, par ^= 1;
+              }
+              if (ok && last) mma_commit<CG>(smem_u32(&sums_full[0]));
+              if (ok && k == 0) ok = mbar_wait(smem_u32(&sums_empty[1]), (n & 1) ^ 1, &failed);
+              if (!ok) break;
+              tc_fence_after();
+              for (uint32_t i = 0; i < run; ++i) {
+                multiply(stage, 1, 1, k + i > 0);
+                mma_commit<CG>(smem_u32(&empty[stage]));
+                if (++stage == S::kStages) stage = 0, parity ^= 1;
+              }
+              if (last) mma_commit<CG>(smem_u32(&sums_full[1]));
+            }
+          }
         }
-        if (ok) mma_commit<CG>(smem_u32(&sums_full[buf]));
       }
     }
   } else {
-    const int mine = warp - 2, quarter = warp & 3;  // quarter: the TMEM lanes that this warp may read
+    if (MH == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int mine = warp - S::kFirst, quarter = warp & 3;  // quarter: the TMEM lanes that this warp may read
     constexpr uint32_t kHalf = BN / 2, kChunks = kHalf / kBox;
     const uint32_t half = (mine >> 2) * kHalf;           // its columns of a tile
     const uint32_t boxes = stages + S::kStages * S::kStageBytes + mine * kBoxes * kBoxBytes;
     const uint32_t bars = smem_u32(&box_full[mine][0]);
-    // The residual boxes of this warp's chunks, brought in order, two ahead; lane 0 only.
-    uint32_t next_t = first, next_c = 0, next_box = 0;
+    // The residual boxes of this warp's chunks, brought in order, kAhead ahead; lane 0 only.
+    uint32_t next_t = first, next_c = 0, next_box = 0;  // next_c: over the chunks of the tile's blocks
+    auto row_of = [&](const Tile& at, uint32_t half) { return ((at.m * CG + rank) * MH + half) * kTileM + quarter * 32; };
     auto fetch = [&]() {
       if (next_t >= p.tiles) return;
       const Tile at = tile_at(p, next_t);
       mbar_expect(bars + 8 * next_box, kBoxBytes);
-      tma_load<false>(boxes + next_box * kBoxBytes, &map_residual, (int)(at.n * BN + half + next_c * kBox),
-                      (int)((at.m * CG + rank) * kTileM) + quarter * 32, (int)at.batch, bars + 8 * next_box);
+      tma_load<false>(boxes + next_box * kBoxBytes, &map_residual, (int)(at.n * BN + half + next_c % kChunks * kBox),
+                      (int)row_of(at, next_c / kChunks), (int)at.batch, bars + 8 * next_box);
       next_box = (next_box + 1) % kBoxes;
-      if (++next_c == kChunks) next_c = 0, next_t += step;
+      if (++next_c == MH * kChunks) next_c = 0, next_t += step;
     };
-    if (p.has_residual && lane == 0) fetch(), fetch();
-    uint32_t n = 0, chunk = 0;
+    if (p.has_residual && lane == 0)
+      for (int i = 0; i < kAhead; ++i) fetch();
+    uint32_t chunk = 0;
     bool ok = true;
-    for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
+    for (uint32_t n = 0;; ++n) {  // blocks of rows: MH to a tile
+      const uint32_t t = first + n / MH * step;
+      if (!ok || t >= p.tiles) break;
       const uint32_t acc = n & 1, round = (n >> 1) & 1;
       if (!(ok = mbar_wait(smem_u32(&sums_full[acc]), round, &failed))) break;
       __syncwarp();
       tc_fence_after();
       const Tile at = tile_at(p, t);
-      const uint32_t row0 = (at.m * CG + rank) * kTileM + quarter * 32;
+      const uint32_t row0 = row_of(at, n % MH);
       const bool live = row0 + lane < p.batch_rows;
       const RowOut r = row_out(p, live ? at.batch * p.batch_rows + row0 + lane : 0u);
       const uint32_t n0 = at.n * BN + half;
+      // MH = 2: all sums are read at once, since the next tile's products wait for their place (with
+      // a read per chunk a seventh of the time); MH = 1: a chunk at a time, the other tile's run.
+      constexpr uint32_t kHeld = MH == 2 ? kChunks : 1;
+      float v[kHeld][kBox];
+      auto read = [&](uint32_t c, float (&to)[kBox]) { tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + half + c * kBox, to); };
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to(smem_u32(&sums_empty[acc]), 0));
+      };
+      if (MH == 2) {
+#pragma unroll
+        for (uint32_t c = 0; c < kHeld; ++c) read(c, v[c]);
+        tmem_wait();
+        release();
+      }
 #pragma unroll 1
       for (uint32_t c = 0; c < kChunks; ++c, ++chunk) {
         const uint32_t buf = chunk % kBoxes;
         Columns<FP8, FP16> columns;
         columns.load(p, r, n0 + c * kBox);
-        float v[32];
-        tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + half + c * kBox, v);
+        if (MH == 1) read(c, v[0]);
         if (lane == 0) {
           if (p.has_residual) {
-            tma_stores_read<1>();  // of the box two chunks ago: the residual two ahead goes there
+            tma_stores_read<kBoxes - kAhead - 1>();  // of the box that takes the residual kAhead ahead
             fetch();
           } else {
             tma_stores_read<kBoxes - 1>();  // of this box
           }
         }
-        tmem_wait();
-        if (c + 1 == kChunks) {  // the sums are in registers: the next tile may have their place
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_to(smem_u32(&sums_empty[acc]), 0));
+        if (MH == 1) {
+          tmem_wait();
+          if (c + 1 == kChunks) release();  // the sums are in registers: the next tile may have their place
         }
         if (p.has_residual && !(ok = mbar_wait(bars + 8 * buf, (chunk / kBoxes) & 1, &failed))) break;
         __syncwarp();
@@ -341,17 +410,24 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
           for (int i = 0; i < 4; ++i)
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(e[i].x), "=r"(e[i].y), "=r"(e[i].z), "=r"(e[i].w) : "r"(piece(i)) : "memory");
         }
-        columns.finish(p, r, v, e);
+        columns.finish(p, r, v[0], e);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(piece(i)), "r"(e[i].x), "r"(e[i].y), "r"(e[i].z), "r"(e[i].w) : "memory");
         fence_for_tma();
         __syncwarp();
-        if (lane == 0 && row0 < p.batch_rows && n0 + c * kBox < p.N)
-          tma_store(&map_out, boxes + buf * kBoxBytes, (int)(n0 + c * kBox), (int)row0, (int)at.batch);
+        if (lane == 0) {
+          if (row0 < p.batch_rows && n0 + c * kBox < p.N)
+            tma_store(&map_out, boxes + buf * kBoxBytes, (int)(n0 + c * kBox), (int)row0, (int)at.batch);
+          tma_stores_commit();  // a group to every box, stored or not
+        }
+#pragma unroll
+        for (uint32_t i = 1; i < kHeld; ++i)  // the next chunk's sums move up: one copy of the loop serves all
+#pragma unroll
+          for (int j = 0; j < kBox; ++j) v[i - 1][j] = v[i][j];
       }
     }
-    if (lane == 0) tma_stores_done();
+    if (lane == 0) tma_stores_read<0>();  // shared memory stays until then; the writes end with the grid
   }
   if (failed && threadIdx.x % 32 == 0) {  // leave copies in flight the time to land
     const uint64_t start = now_ns();
@@ -365,6 +441,167 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
   if (warp == 1) {
     tc_fence_after();
     tmem_free<CG>(tmem, S::kColumns);
+  }
+}
+
+// ---- few tiles: the sum over K split over a cluster ------------------------------------------
+//
+// Where there are fewer tiles than SMs, reading x and W through the few that have one sets the
+// pace (an SM takes some 80 bytes a cycle). S groups of CG CTAs, a cluster, take a tile together,
+// each an S-th of K; then each group finishes an S-th of the tile's 32-column chunks, to which
+// the others add their sums: they write them to its shared memory, over the stages.
+
+template <int CG, int BN>
+struct SplitShape {
+  static constexpr int kStageBytes = (kTileM + BN / CG) * kStepBytes;
+  static constexpr int kFit = 225 * 1024 / kStageBytes, kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr int kShared = kStages * kStageBytes + 1024;
+  static constexpr int kChunks = BN / kBox;
+  static constexpr int kThreads = 32 * (2 + kEpilogueWarps);
+  // Sums that a CTA receives: from each other group, for each of its chunks.
+  static constexpr int received(int S) { return (S - 1) * ((kChunks + S - 1) / S) * kTileM * kBox * 4; }
+};
+
+template <int CG, int BN, bool FP8, bool FP16>
+__global__ void __launch_bounds__(SplitShape<CG, BN>::kThreads, 1)
+linear_gate_split(const __grid_constant__ LinearParams p, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w) {
+  using Shape = SplitShape<CG, BN>;
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t full[Shape::kStages], empty[Shape::kStages], sums_full;
+  __shared__ uint32_t tmem_at;
+  __shared__ int failed;
+  const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank(), size = cluster_size();
+  const uint32_t S = size / CG, mine = rank / CG, side = rank % CG, leader = rank - side;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Shape::kStages; ++i) mbar_init(smem_u32(&full[i]), 1), mbar_init(smem_u32(&empty[i]), 1);
+    mbar_init(smem_u32(&sums_full), 1);
+    failed = 0;
+    mbar_init_fence();
+  }
+  if (threadIdx.x == 64) {
+    prefetch_map(&map_x);
+    prefetch_map(&map_w);
+  }
+  if (warp == 1) tmem_alloc<CG>(smem_u32(&tmem_at), BN);
+  __syncthreads();
+  if (CG == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *(volatile uint32_t*)&tmem_at;
+
+  const Tile at = tile_at(p, blockIdx.x / size);
+  const uint32_t k0 = mine * p.steps / S, k1 = (mine + 1) * p.steps / S;  // S <= steps
+  if (warp == 0) {
+    if (elect_one()) {
+      constexpr int kElems = FP8 ? 128 : 64;
+      const int row = (int)((at.m * CG + side) * kTileM), col = (int)(at.n * BN + side * (BN / CG));
+      uint32_t stage = 0, parity = 0;
+      for (uint32_t k = k0; k < k1; ++k) {
+        if (!mbar_wait(smem_u32(&empty[stage]), parity ^ 1, &failed)) break;
+        uint32_t bar = smem_u32(&full[stage]);
+        if (side == 0) mbar_expect(bar, CG * Shape::kStageBytes);
+        if (CG == 2) bar = map_to(bar, leader);
+        const uint32_t a = stages + stage * Shape::kStageBytes;
+        tma_load<CG == 2>(a, &map_x, (int)k * kElems, row, (int)at.batch, bar);
+        tma_load<CG == 2>(a + kTileM * kStepBytes, &map_w, (int)k * kElems, col, 0, bar);
+        if (++stage == Shape::kStages) stage = 0, parity ^= 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (side == 0 && elect_one()) {
+      uint32_t stage = 0, parity = 0;
+      bool ok = true;
+      for (uint32_t k = k0; k < k1; ++k) {
+        if (!(ok = mbar_wait(smem_u32(&full[stage]), parity, &failed))) break;
+        tc_fence_after();
+        const uint32_t a = stages + stage * Shape::kStageBytes;
+        const uint64_t da = operand_desc(a), db = operand_desc(a + kTileM * kStepBytes);
+#pragma unroll
+        for (int i = 0; i < kStepBytes / 32; ++i) mma<CG, FP8>(tmem, da + 2 * i, db + 2 * i, p.idesc, k > k0 || i > 0);
+        mma_commit<CG>(smem_u32(&empty[stage]), leader);
+        if (++stage == Shape::kStages) stage = 0, parity ^= 1;
+      }
+      if (ok) mma_commit<CG>(smem_u32(&sums_full), leader);
+    }
+  } else {
+    mbar_wait(smem_u32(&sums_full), 0, &failed);  // every product is done, and every copy has been used
+    tc_fence_after();
+  }
+  __syncwarp();
+  cluster_sync();  // now no stage of the cluster is in use
+
+  constexpr uint32_t kHalf = Shape::kChunks / 2;
+  const int quarter = warp & 3;
+  const uint32_t first = warp >= 2 ? (uint32_t)(warp - 2) / 4 * kHalf : 0u;  // this warp's chunks
+  const uint32_t each = (Shape::kChunks + S - 1) / S;                       // chunks of a group, at most
+  auto owner_of = [&](uint32_t j) { return j * S / Shape::kChunks; };
+  auto first_of = [&](uint32_t o) { return (o * Shape::kChunks + S - 1) / S; };
+  auto slot = [&](uint32_t from, uint32_t to, uint32_t j) {  // of sums for chunk j, from one group to another
+    return stages + ((((from < to ? from : from - 1) * each + (j - first_of(to))) * 4 + quarter) * 8 * 32 + lane) * 16;
+  };
+  const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+  if (warp >= 2) {
+    for (uint32_t j = first; j < first + kHalf; ++j) {
+      const uint32_t to = owner_of(j);
+      if (to == mine) continue;
+      float v[kBox];
+      tmem_load32(lanes + j * kBox, v);
+      const uint32_t there = map_to(slot(mine, to, j), to * CG + side);
+      tmem_wait();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) store_remote(there + i * 512, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+  }
+  cluster_sync();
+  if (warp >= 2) {
+    const uint32_t row0 = (at.m * CG + side) * kTileM + quarter * 32;
+    const bool live = row0 + lane < p.batch_rows;
+    const RowOut r = row_out(p, live ? at.batch * p.batch_rows + row0 + lane : 0u);
+    const uint16_t* res = p.residual.ptr + (r.b * p.residual.sb + r.l * p.residual.sl);
+    uint16_t* out = p.out + (r.b * p.out_sb + r.l * p.out_sl);
+    for (uint32_t j = first; j < first + kHalf; ++j) {
+      if (owner_of(j) != mine) continue;
+      const uint32_t n0 = at.n * BN + j * kBox;
+      Columns<FP8, FP16> columns;
+      columns.load(p, r, n0);
+      uint4 e[4];
+      auto here_too = [&](int i) { return live && n0 + 8 * i < p.N; };
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (p.has_residual && here_too(i)) e[i] = *reinterpret_cast<const uint4*>(res + n0 + 8 * i);
+      float v[kBox];
+      tmem_load32(lanes + j * kBox, v);
+      tmem_wait();
+      for (uint32_t from = 0; from < S; ++from) {  // in the order of K's parts, after its own
+        if (from == mine) continue;
+        const uint32_t here = slot(from, mine, j);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float a, b, c, d;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a), "=f"(b), "=f"(c), "=f"(d) : "r"(here + i * 512) : "memory");
+          v[4 * i] += a, v[4 * i + 1] += b, v[4 * i + 2] += c, v[4 * i + 3] += d;
+        }
+      }
+      columns.finish(p, r, v, e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (here_too(i)) *reinterpret_cast<uint4*>(out + n0 + 8 * i) = e[i];
+    }
+  }
+  if (failed && lane == 0) {  // leave copies in flight the time to land
+    const uint64_t start = now_ns();
+    while (now_ns() - start < 1000000000ull) __nanosleep(1000000);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();
+  if (threadIdx.x == 0 && failed) atomicAdd(&linear_gate_gave_up, 1);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free<CG>(tmem, BN);
   }
 }
 

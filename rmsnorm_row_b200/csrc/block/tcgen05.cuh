@@ -23,6 +23,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return n;
+}
+// 16 bytes to shared memory of a CTA of the cluster (an address from map_to).
+__device__ __forceinline__ void store_remote(uint32_t to, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
 // A shared-memory address of this CTA as the same place in the cluster's CTA `rank`.
 __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -102,13 +111,13 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* m, uint32_t from, i
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m), "r"(x), "r"(y),
                "r"(z), "r"(from)
                : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+// Closes the group of stores since the last call, which may be none: the waits below count groups.
+__device__ __forceinline__ void tma_stores_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 template <int LEFT>
 __device__ __forceinline__ void tma_stores_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
 }
-__device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // This thread's writes to shared memory before TMA's reads of it.
 __device__ __forceinline__ void fence_for_tma() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -158,14 +167,15 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
   }
 #undef BLOCK_OPS_MMA
 }
-// Arrives on `bar` (of both CTAs for a pair) when the products issued so far are done.
+// Arrives on `bar` (of both CTAs of a pair, whose even rank in the cluster is `leader`) when the
+// products issued so far are done.
 template <int CG>
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t leader = 0) {
   if (CG == 1)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
   else
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                 "h"((uint16_t)3)
+                 "h"((uint16_t)(3u << leader))
                  : "memory");
 }
 // 32 columns of this warp's 32 lanes; the values are there after tmem_wait.

@@ -147,6 +147,40 @@ def test_against_the_formula(case):
     assert timeouts() == 0
 
 
+# Few tiles, where K is split over a cluster: two to eight parts, pairs of CTAs, parts that own one
+# chunk of columns or none, K that does not divide; rows of batches apart. And a 512-row tile.
+SPLIT = [
+    (1, 999, 2056, 1288, HF, 0, "silu", True, "none", False),
+    (3, 333, 2056, 1288, BF, 0, "none", True, "batch", True),
+    (1, 64, 5120, 5120, BF, 0, "none", True, "bcast", True),
+    (1, 5, 12288, 512, HF, 0, "gelu", True, "vec", True),
+    (1, 130, 1000, 64, BF, 0, "none", False, "row", True),
+    (1, 100, 4096, 8, BF, 0, "none", True, "none", True),
+    (1, 512, 11000, 264, HF, 0, "silu", False, "none", False),
+    (2, 300, 2048, 2048, F8, 3, "gelu_tanh", True, "frame", True),
+    (1, 31, 16384, 1032, F8, 0, "none", True, "none", True),
+    (1, 700, 256, 600, F8, 0, "none", True, "row", False),
+    (1, 1500, 3000, 1000, BF, 0, "gelu_tanh", True, "none", True),
+    (1, 9, 520, 520, HF, 0, "none", True, "none", False),
+    (1, 37800, 4096, 512, BF, 21, "silu", True, "frame", True),
+    (1, 37800, 4104, 520, HF, 0, "none", False, "none", False),
+]
+
+
+@pytest.mark.parametrize("case", SPLIT, ids=lambda c: "-".join(str(v).replace("torch.", "") for v in c))
+def test_split_sums_and_long_tiles(case):
+    B, L, K, N, dtype, F, act, bias, gate, residual = case
+    before = timeouts()
+    t = make(B, L, K, N, dtype, F, bias, gate, residual, seed=300)
+    out = call(t, act)
+    check(out, t, act)
+    bits = out.view(torch.int16)  # a NaN's too
+    assert torch.equal(bits, call(t, act).view(torch.int16))
+    if residual:  # in place
+        assert torch.equal(call(t, act, out=t["residual"]).view(torch.int16), bits)
+    assert timeouts() == before
+
+
 @pytest.mark.parametrize("L", [3, 200])
 @pytest.mark.parametrize("dtype", [BF, F8])
 def test_strided_rows_outputs_and_in_place(L, dtype):
