@@ -136,7 +136,8 @@ Variant variant() {
                  {(void*)linear_gate_tiles<CG, MH, BN, false, false>, (void*)linear_gate_tiles<CG, MH, BN, false, true>,
                   MH == 2 ? nullptr : (void*)linear_gate_tiles<CG, 1, BN, true, false>}};
 }
-const Variant kVariants[] = {variant<2, 2, 256>(), variant<2, 1, 256>(), variant<1, 1, 256>(), variant<1, 1, 128>(), variant<1, 1, 64>()};
+const Variant kVariants[] = {variant<2, 2, 256>(), variant<2, 1, 256>(), variant<2, 1, 192>(), variant<2, 1, 128>(),
+                             variant<1, 1, 256>(), variant<1, 1, 128>(), variant<1, 1, 64>()};
 
 template <int CG, int BN>
 Variant split_variant() {

@@ -187,7 +187,7 @@ struct MatrixShape {
   // Loading, products, then the epilogue's warps. With MH = 2 these are warpgroups of their own,
   // which take over registers of the first: 40 + 2 x 232 of the 3 x 168 at launch.
   static constexpr int kFirst = MH == 2 ? 4 : 2, kThreads = 32 * (kFirst + kEpilogueWarps);
-  static constexpr int kColumns = 2 * BN;  // TMEM: two blocks of sums
+  static constexpr int kColumns = BN == 192 ? 512 : 2 * BN;  // TMEM, a power of two: two blocks of sums
   static constexpr int kShared = kStages * kStageBytes + kBoxesBytes + 1024;  // 1024: alignment
 };
 
