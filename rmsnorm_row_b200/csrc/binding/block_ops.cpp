@@ -167,16 +167,28 @@ PyObject* wrap(PyObject* given, const Tensor& t) {
   return THPVariable_Wrap(t);
 }
 
-// The caller's stream on x's device: a torch.cuda.Stream, or None for the current one.
-fn_stream_t stream_of(PyObject* o, const at::Device& device) {
-  if (o == Py_None) return reinterpret_cast<fn_stream_t>(c10::cuda::getCurrentCUDAStream(device.index()).stream());
-  PyObject* v = PyObject_GetAttrString(o, "cuda_stream");
-  if (!v) throw Raised();
-  void* s = PyLong_AsVoidPtr(v);
-  Py_DECREF(v);
-  if (PyErr_Occurred()) throw Raised();
-  return reinterpret_cast<fn_stream_t>(s);
-}
+// The device and stream of a call: x's device, and the caller's torch.cuda.Stream or the current
+// one. Outputs and workspace come from that stream's memory, which no other stream is using.
+class Place {
+ public:
+  Place(PyObject* stream, const at::Device& device) : device_(device) {
+    if (stream != Py_None) {
+      PyObject* v = PyObject_GetAttrString(stream, "cuda_stream");
+      if (!v) throw Raised();
+      void* s = PyLong_AsVoidPtr(v);
+      Py_DECREF(v);
+      if (PyErr_Occurred()) throw Raised();
+      stream_.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), device.index()));
+    }
+    handle_ = reinterpret_cast<fn_stream_t>(c10::cuda::getCurrentCUDAStream(device.index()).stream());
+  }
+  fn_stream_t stream() const { return handle_; }
+
+ private:
+  const c10::cuda::CUDAGuard device_;
+  c10::cuda::OptionalCUDAStreamGuard stream_;
+  fn_stream_t handle_;
+};
 
 // One handle per configuration and process. Configurations are zeroed before they are filled,
 // so their bytes compare; the interpreter's lock guards the list.
@@ -251,7 +263,7 @@ ENTRY(norm_quant, 13) {
   if (weight && bias && weight->scalar_type() != bias->scalar_type()) throw TypeError("weight and bias must have the same dtype");
   c.affine_fp32 = (weight && weight->scalar_type() == at::kFloat) || (bias && bias->scalar_type() == at::kFloat);
 
-  const c10::cuda::CUDAGuard guard(device);
+  const Place place(a[12], device);
   Tensor r, q, s;
   if (residual) {
     check_tensor(*residual, "residual", device, bf);
@@ -271,7 +283,7 @@ ENTRY(norm_quant, 13) {
   g.q = q.data_ptr(), g.q_stride_b = q.stride(0), g.q_stride_l = q.stride(1);
   g.row_scale = static_cast<float*>(s.data_ptr());
   const norm_quant_t h = handle_for(c, norm_quant_create, "norm_quant_create");
-  check_status(norm_quant_launch(h, &g, stream_of(a[12], device)), "norm_quant_launch");
+  check_status(norm_quant_launch(h, &g, place.stream()), "norm_quant_launch");
   PyObject* out = PyTuple_New(residual ? 3 : 2);
   if (!out) throw Raised();
   PyTuple_SET_ITEM(out, 0, wrap(a[9], q));
@@ -363,12 +375,12 @@ ENTRY(rope_norm, 11) {
   rn_args g = zeroed<rn_args>();
   g.x = heads_of(x, "x", nullptr);
   const RopeCall call = rope_call(x, a + 1);
-  const c10::cuda::CUDAGuard guard(x.device());
+  const Place place(a[10], x.device());
   const Tensor y = a[9] == Py_None ? empty(x.sizes(), x.scalar_type(), x.device()) : *tensor(a[9], "out");
   g.B = x.size(0), g.L = x.size(1);
   g.positions = call.positions, g.pos_stride_b = call.psb, g.pos_stride_l = call.psl, g.weight = call.weight;
   g.y = heads_of(y, "out", &x);
-  check_status(rope_norm_launch(call.h, &g, stream_of(a[10], x.device())), "rope_norm_launch");
+  check_status(rope_norm_launch(call.h, &g, place.stream()), "rope_norm_launch");
   return wrap(a[9], y);
 }
 
@@ -381,12 +393,11 @@ ENTRY(rope_norm_backward, 12) {
   g.grad = heads_of(grad, "grad", &x);
   const RopeCall call = rope_call(x, a + 2);
   if (choice(a[8], "norm", {"none", "head", "all"}) == BO_NORM_NONE) g.x = rn_rows{nullptr, 0, 0, 0};
-  const c10::cuda::CUDAGuard guard(x.device());
+  const Place place(a[11], x.device());
   const Tensor dx = a[10] == Py_None ? empty(x.sizes(), x.scalar_type(), x.device()) : *tensor(a[10], "out");
   g.B = x.size(0), g.L = x.size(1);
   g.positions = call.positions, g.pos_stride_b = call.psb, g.pos_stride_l = call.psl, g.weight = call.weight;
   g.dx = heads_of(dx, "out", &x);
-  const fn_stream_t stream = stream_of(a[11], x.device());
   Tensor dw, work;
   if (call.weight) {
     const Tensor& w = THPVariable_Unpack(a[4]);
@@ -395,11 +406,8 @@ ENTRY(rope_norm_backward, 12) {
     work = empty({(int64_t)g.workspace_bytes}, at::kByte, x.device());
     g.dweight = static_cast<float*>(dw.data_ptr());
     g.workspace = g.workspace_bytes ? work.data_ptr() : nullptr;
-    if (a[11] != Py_None && g.workspace)  // dropped on return, in use on that stream
-      c10::cuda::CUDACachingAllocator::recordStream(
-          work.storage().data_ptr(), c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), x.device().index()));
   }
-  check_status(rope_norm_backward_launch(call.h, &g, stream), "rope_norm_backward_launch");
+  check_status(rope_norm_backward_launch(call.h, &g, place.stream()), "rope_norm_backward_launch");
   PyObject* out = PyTuple_New(2);
   if (!out) throw Raised();
   PyTuple_SET_ITEM(out, 0, wrap(a[10], dx));
@@ -453,13 +461,13 @@ ENTRY(linear_gate, 10) {
     check_tensor(*residual, "residual", device, dtype);
     g.residual = rows_of(*residual);
   }
-  const c10::cuda::CUDAGuard guard(device);
+  const Place place(a[9], device);
   const Tensor out = a[8] == Py_None ? empty({B, L, N}, dtype, device) : *tensor(a[8], "out");
   check_shape(out, "out", {B, L, N}, dtype, device);
   check_tensor(out, "out", device, dtype);
   g.out = out.data_ptr(), g.out_stride_b = out.stride(0), g.out_stride_l = out.stride(1);
   const linear_gate_t h = handle_for(c, linear_gate_create, "linear_gate_create");
-  check_status(linear_gate_launch(h, &g, stream_of(a[9], device)), "linear_gate_launch");
+  check_status(linear_gate_launch(h, &g, place.stream()), "linear_gate_launch");
   return wrap(a[8], out);
 }
 
