@@ -126,13 +126,13 @@ fn_status launch_tokens(const linear_gate_s* h, LinearParams& p, cudaStream_t st
 // ---- many rows --------------------------------------------------------------------------------
 
 struct Variant {
-  int cg, mh, bn, shared, stages, threads, received[9];  // received: bytes of sums by the parts of K, of a split tile
+  int cg, mh, bn, shared, stages, received[9];  // received: bytes of sums by the parts of K, of a split tile
   void* kernel[3];  // by dtype: bf16, fp16, e4m3
   int rows() const { return kTileM * cg * mh; }
 };
 template <int CG, int MH, int BN>
 Variant variant() {
-  return Variant{CG, MH, BN, MatrixShape<CG, MH, BN>::kShared, MatrixShape<CG, MH, BN>::kStages, MatrixShape<CG, MH, BN>::kThreads, {},
+  return Variant{CG, MH, BN, MatrixShape<CG, MH, BN>::kShared, MatrixShape<CG, MH, BN>::kStages, {},
                  {(void*)linear_gate_tiles<CG, MH, BN, false, false>, (void*)linear_gate_tiles<CG, MH, BN, false, true>,
                   MH == 2 ? nullptr : (void*)linear_gate_tiles<CG, 1, BN, true, false>}};
 }
@@ -142,7 +142,7 @@ const Variant kVariants[] = {variant<2, 2, 256>(), variant<2, 1, 256>(), variant
 template <int CG, int BN>
 Variant split_variant() {
   using S = SplitShape<CG, BN>;
-  Variant v{CG, 1, BN, S::kShared, S::kStages, S::kThreads, {},
+  Variant v{CG, 1, BN, S::kShared, S::kStages, {},
             {(void*)linear_gate_split<CG, BN, false, false>, (void*)linear_gate_split<CG, BN, false, true>,
              (void*)linear_gate_split<CG, BN, true, false>}};
   for (int n = 1; n <= 8; ++n) v.received[n] = S::received(n);
@@ -202,7 +202,7 @@ fn_status clusters_at_once(const Variant& v, int n, int dtype, int* count) {
   if (*count) return FN_OK;
   cudaError_t e = cudaFuncSetAttribute(v.kernel[dtype], cudaFuncAttributeMaxDynamicSharedMemorySize, v.shared);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n * v.cg), cfg.blockDim = dim3(v.threads), cfg.dynamicSmemBytes = v.shared;
+  cfg.gridDim = dim3(n * v.cg), cfg.blockDim = dim3(kMatrixThreads), cfg.dynamicSmemBytes = v.shared;
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
   cluster.val.clusterDim.x = n * v.cg, cluster.val.clusterDim.y = 1, cluster.val.clusterDim.z = 1;
@@ -294,7 +294,7 @@ fn_status launch_tiles(const linear_gate_s* h, const lg_args* a, LinearParams& p
   const int64_t resident = sms / v.cg;  // a split tile's CTAs are not persistent
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((tiles < resident || parts > 1 ? tiles : resident) * v.cg * parts));
-  cfg.blockDim = dim3(v.threads);
+  cfg.blockDim = dim3(kMatrixThreads);
   cfg.dynamicSmemBytes = v.shared;
   cfg.stream = stream;
   cudaLaunchAttribute cluster;

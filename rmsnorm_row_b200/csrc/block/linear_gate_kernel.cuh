@@ -172,6 +172,7 @@ constexpr int kTileM = 128;          // rows of a CTA
 constexpr int kStepBytes = 128;      // of K, per row and stage
 constexpr int kMaxStages = 8;
 constexpr int kEpilogueWarps = 8;    // two to each quarter of the rows, each half of the columns
+constexpr int kMatrixThreads = 32 * (2 + kEpilogueWarps);
 constexpr int kBox = 32;             // rows and columns of an output box
 constexpr int kBoxBytes = kBox * kBox * 2;
 
@@ -184,9 +185,6 @@ struct MatrixShape {
   static constexpr int kBoxesBytes = kEpilogueWarps * kBoxes * kBoxBytes;
   static constexpr int kFit = (226 * 1024 - 1024 - kBoxesBytes) / kStageBytes;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-  // Loading, products, then the epilogue's warps. With MH = 2 these are warpgroups of their own,
-  // which take over registers of the first: 40 + 2 x 232 of the 3 x 168 at launch.
-  static constexpr int kFirst = MH == 2 ? 4 : 2, kThreads = 32 * (kFirst + kEpilogueWarps);
   static constexpr int kColumns = BN == 192 ? 512 : 2 * BN;  // TMEM, a power of two: two blocks of sums
   static constexpr int kShared = kStages * kStageBytes + kBoxesBytes + 1024;  // 1024: alignment
 };
@@ -208,7 +206,7 @@ __device__ __forceinline__ Tile tile_at(const LinearParams& p, uint32_t t) {
 __device__ int linear_gate_gave_up = 0;  // launches in which a wait ran out (this file is included once)
 
 template <int CG, int MH, int BN, bool FP8, bool FP16>
-__global__ void __launch_bounds__(MatrixShape<CG, MH, BN>::kThreads, 1)
+__global__ void __launch_bounds__(kMatrixThreads, 1)
 linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant__ CUtensorMap map_x,
                   const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_out,
                   const __grid_constant__ CUtensorMap map_residual) {
@@ -243,96 +241,92 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
   const uint32_t tmem = *(volatile uint32_t*)&tmem_at;
 
   const uint32_t first = blockIdx.x / CG, step = gridDim.x / CG;
-  if (warp < S::kFirst) {
-    if (MH == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 0) {
-      if (elect_one()) {
-        constexpr int kElems = FP8 ? 128 : 64;  // of K, per step
-        uint32_t stage = 0, parity = 0;
-        bool ok = true;
-        for (uint32_t t = first; ok && t < p.tiles; t += step) {
-          const Tile at = tile_at(p, t);
-          const int row = (int)((at.m * CG + rank) * MH * kTileM), col = (int)(at.n * BN + rank * (BN / CG));
-          for (uint32_t k = 0; k < p.steps; ++k) {
-            if (!(ok = mbar_wait(smem_u32(&empty[stage]), parity ^ 1, &failed))) break;
-            uint32_t bar = smem_u32(&full[stage]);
-            if (rank == 0) mbar_expect(bar, CG * S::kStageBytes);
-            if (CG == 2) bar = map_to(bar, 0);
-            const uint32_t a = stages + stage * S::kStageBytes;
-            tma_load<CG == 2>(a, &map_x, (int)k * kElems, row, (int)at.batch, bar);
-            tma_load<CG == 2>(a + S::kABytes, &map_w, (int)k * kElems, col, 0, bar);
-            if (++stage == S::kStages) stage = 0, parity ^= 1;
-          }
-        }
-        // The last copies have landed when their stages are free again.
-        for (int i = 0; ok && i < S::kStages; ++i) {
-          ok = mbar_wait(smem_u32(&empty[stage]), parity ^ 1, &failed);
+  if (warp == 0) {
+    if (elect_one()) {
+      constexpr int kElems = FP8 ? 128 : 64;  // of K, per step
+      uint32_t stage = 0, parity = 0;
+      bool ok = true;
+      for (uint32_t t = first; ok && t < p.tiles; t += step) {
+        const Tile at = tile_at(p, t);
+        const int row = (int)((at.m * CG + rank) * MH * kTileM), col = (int)(at.n * BN + rank * (BN / CG));
+        for (uint32_t k = 0; k < p.steps; ++k) {
+          if (!(ok = mbar_wait(smem_u32(&empty[stage]), parity ^ 1, &failed))) break;
+          uint32_t bar = smem_u32(&full[stage]);
+          if (rank == 0) mbar_expect(bar, CG * S::kStageBytes);
+          if (CG == 2) bar = map_to(bar, 0);
+          const uint32_t a = stages + stage * S::kStageBytes;
+          tma_load<CG == 2>(a, &map_x, (int)k * kElems, row, (int)at.batch, bar);
+          tma_load<CG == 2>(a + S::kABytes, &map_w, (int)k * kElems, col, 0, bar);
           if (++stage == S::kStages) stage = 0, parity ^= 1;
         }
       }
-    } else if (warp == 1) {
-      if (rank == 0 && elect_one()) {
-        uint32_t stage = 0, parity = 0, n = 0;
-        bool ok = true;
-        // The products of block `half` with stage s into its sums.
-        auto multiply = [&](uint32_t s, uint32_t acc, int half, bool add) {
-          const uint32_t a = stages + s * S::kStageBytes;
-          const uint64_t da = operand_desc(a + half * kTileM * kStepBytes), db = operand_desc(a + S::kABytes);
+      // The last copies have landed when their stages are free again.
+      for (int i = 0; ok && i < S::kStages; ++i) {
+        ok = mbar_wait(smem_u32(&empty[stage]), parity ^ 1, &failed);
+        if (++stage == S::kStages) stage = 0, parity ^= 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one()) {
+      uint32_t stage = 0, parity = 0, n = 0;
+      bool ok = true;
+      // The products of block `half` with stage s into its sums.
+      auto multiply = [&](uint32_t s, uint32_t acc, int half, bool add) {
+        const uint32_t a = stages + s * S::kStageBytes;
+        const uint64_t da = operand_desc(a + half * kTileM * kStepBytes), db = operand_desc(a + S::kABytes);
 #pragma unroll
-          for (int i = 0; i < kStepBytes / 32; ++i)  // 32 bytes of K each
-            mma<CG, FP8>(tmem + acc * BN, da + 2 * i, db + 2 * i, p.idesc, add || i > 0);
-        };
-        auto wait_full = [&](uint32_t s, uint32_t par) {
-          const bool got = mbar_wait(smem_u32(&full[s]), par, &failed);
+        for (int i = 0; i < kStepBytes / 32; ++i)  // 32 bytes of K each
+          mma<CG, FP8>(tmem + acc * BN, da + 2 * i, db + 2 * i, p.idesc, add || i > 0);
+      };
+      auto wait_full = [&](uint32_t s, uint32_t par) {
+        const bool got = mbar_wait(smem_u32(&full[s]), par, &failed);
+        tc_fence_after();
+        return got;
+      };
+      if (MH == 1) {
+        for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
+          const uint32_t buf = n & 1, round = (n >> 1) & 1;
+          if (!(ok = mbar_wait(smem_u32(&sums_empty[buf]), round ^ 1, &failed))) break;
           tc_fence_after();
-          return got;
-        };
-        if (MH == 1) {
-          for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
-            const uint32_t buf = n & 1, round = (n >> 1) & 1;
-            if (!(ok = mbar_wait(smem_u32(&sums_empty[buf]), round ^ 1, &failed))) break;
+          for (uint32_t k = 0; k < p.steps; ++k) {
+            if (!(ok = wait_full(stage, parity))) break;
+            multiply(stage, buf, 0, k > 0);
+            mma_commit<CG>(smem_u32(&empty[stage]));
+            if (++stage == S::kStages) stage = 0, parity ^= 1;
+          }
+          if (ok) mma_commit<CG>(smem_u32(&sums_full[buf]));
+        }
+      } else {
+        // Runs of stages, first block 0 and then block 1: long ones at a tile's ends, so that the
+        // sums of one block are read out while the other's products run; a stage elsewhere.
+        const uint32_t most = S::kStages - 1, ends = p.steps / 2 < most ? p.steps / 2 : most;
+        for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
+          for (uint32_t k = 0, run; ok && k < p.steps; k += run) {
+            run = (k == 0 || k + ends == p.steps) && ends > 1 ? ends : 1;
+            const bool last = k + run == p.steps;
+            uint32_t s = stage, par = parity;
+            if (k == 0) ok = mbar_wait(smem_u32(&sums_empty[0]), (n & 1) ^ 1, &failed);
+            for (uint32_t i = 0; ok && i < run; ++i) {
+              if (!(ok = wait_full(s, par))) break;
+              multiply(s, 0, 0, k + i > 0);
+              if (++s == S::kStages) s = 0, par ^= 1;
+            }
+            if (ok && last) mma_commit<CG>(smem_u32(&sums_full[0]));
+            if (ok && k == 0) ok = mbar_wait(smem_u32(&sums_empty[1]), (n & 1) ^ 1, &failed);
+            if (!ok) break;
             tc_fence_after();
-            for (uint32_t k = 0; k < p.steps; ++k) {
-              if (!(ok = wait_full(stage, parity))) break;
-              multiply(stage, buf, 0, k > 0);
+            for (uint32_t i = 0; i < run; ++i) {
+              multiply(stage, 1, 1, k + i > 0);
               mma_commit<CG>(smem_u32(&empty[stage]));
               if (++stage == S::kStages) stage = 0, parity ^= 1;
             }
-            if (ok) mma_commit<CG>(smem_u32(&sums_full[buf]));
-          }
-        } else {
-          // Runs of stages, first block 0 and then block 1: long ones at a tile's ends, so that the
-          // sums of one block are read out while the other's products run; a stage elsewhere.
-          const uint32_t most = S::kStages - 1, ends = p.steps / 2 < most ? p.steps / 2 : most;
-          for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
-            for (uint32_t k = 0, run; ok && k < p.steps; k += run) {
-              run = (k == 0 || k + ends == p.steps) && ends > 1 ? ends : 1;
-              const bool last = k + run == p.steps;
-              uint32_t s = stage, par = parity;
-              if (k == 0) ok = mbar_wait(smem_u32(&sums_empty[0]), (n & 1) ^ 1, &failed);
-              for (uint32_t i = 0; ok && i < run; ++i) {
-                if (!(ok = wait_full(s, par))) break;
-                multiply(s, 0, 0, k + i > 0);
-                if (++s == S::kStages) s = 0, par ^= 1;
-              }
-              if (ok && last) mma_commit<CG>(smem_u32(&sums_full[0]));
-              if (ok && k == 0) ok = mbar_wait(smem_u32(&sums_empty[1]), (n & 1) ^ 1, &failed);
-              if (!ok) break;
-              tc_fence_after();
-              for (uint32_t i = 0; i < run; ++i) {
-                multiply(stage, 1, 1, k + i > 0);
-                mma_commit<CG>(smem_u32(&empty[stage]));
-                if (++stage == S::kStages) stage = 0, parity ^= 1;
-              }
-              if (last) mma_commit<CG>(smem_u32(&sums_full[1]));
-            }
+            if (last) mma_commit<CG>(smem_u32(&sums_full[1]));
           }
         }
       }
     }
   } else {
-    if (MH == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-    const int mine = warp - S::kFirst, quarter = warp & 3;  // quarter: the TMEM lanes that this warp may read
+    const int mine = warp - 2, quarter = warp & 3;  // quarter: the TMEM lanes that this warp may read
     constexpr uint32_t kHalf = BN / 2, kChunks = kHalf / kBox;
     const uint32_t half = (mine >> 2) * kHalf;           // its columns of a tile
     const uint32_t boxes = stages + S::kStages * S::kStageBytes + mine * kBoxes * kBoxBytes;
@@ -365,28 +359,13 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
       const bool live = row0 + lane < p.batch_rows;
       const RowOut r = row_out(p, live ? at.batch * p.batch_rows + row0 + lane : 0u);
       const uint32_t n0 = at.n * BN + half;
-      // MH = 2: all sums are read at once, since the next tile's products wait for their place (with
-      // a read per chunk a seventh of the time); MH = 1: a chunk at a time, the other tile's run.
-      constexpr uint32_t kHeld = MH == 2 ? kChunks : 1;
-      float v[kHeld][kBox];
-      auto read = [&](uint32_t c, float (&to)[kBox]) { tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + half + c * kBox, to); };
-      auto release = [&]() {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_to(smem_u32(&sums_empty[acc]), 0));
-      };
-      if (MH == 2) {
-#pragma unroll
-        for (uint32_t c = 0; c < kHeld; ++c) read(c, v[c]);
-        tmem_wait();
-        release();
-      }
 #pragma unroll 1
       for (uint32_t c = 0; c < kChunks; ++c, ++chunk) {
         const uint32_t buf = chunk % kBoxes;
         Columns<FP8, FP16> columns;
         columns.load(p, r, n0 + c * kBox);
-        if (MH == 1) read(c, v[0]);
+        float v[kBox];
+        tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + half + c * kBox, v);
         if (lane == 0) {
           if (p.has_residual) {
             tma_stores_read<kBoxes - kAhead - 1>();  // of the box that takes the residual kAhead ahead
@@ -395,9 +374,11 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
             tma_stores_read<kBoxes - 1>();  // of this box
           }
         }
-        if (MH == 1) {
-          tmem_wait();
-          if (c + 1 == kChunks) release();  // the sums are in registers: the next tile may have their place
+        tmem_wait();
+        if (c + 1 == kChunks) {  // the sums are in registers: the next tile may have their place
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to(smem_u32(&sums_empty[acc]), 0));
         }
         if (p.has_residual && !(ok = mbar_wait(bars + 8 * buf, (chunk / kBoxes) & 1, &failed))) break;
         __syncwarp();
@@ -410,7 +391,7 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
           for (int i = 0; i < 4; ++i)
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(e[i].x), "=r"(e[i].y), "=r"(e[i].z), "=r"(e[i].w) : "r"(piece(i)) : "memory");
         }
-        columns.finish(p, r, v[0], e);
+        columns.finish(p, r, v, e);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(piece(i)), "r"(e[i].x), "r"(e[i].y), "r"(e[i].z), "r"(e[i].w) : "memory");
@@ -421,10 +402,6 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
             tma_store(&map_out, boxes + buf * kBoxBytes, (int)(n0 + c * kBox), (int)row0, (int)at.batch);
           tma_stores_commit();  // a group to every box, stored or not
         }
-#pragma unroll
-        for (uint32_t i = 1; i < kHeld; ++i)  // the next chunk's sums move up: one copy of the loop serves all
-#pragma unroll
-          for (int j = 0; j < kBox; ++j) v[i - 1][j] = v[i][j];
       }
     }
     if (lane == 0) tma_stores_read<0>();  // shared memory stays until then; the writes end with the grid
@@ -457,13 +434,12 @@ struct SplitShape {
   static constexpr int kFit = 225 * 1024 / kStageBytes, kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kShared = kStages * kStageBytes + 1024;
   static constexpr int kChunks = BN / kBox;
-  static constexpr int kThreads = 32 * (2 + kEpilogueWarps);
   // Sums that a CTA receives: from each other group, for each of its chunks.
   static constexpr int received(int S) { return (S - 1) * ((kChunks + S - 1) / S) * kTileM * kBox * 4; }
 };
 
 template <int CG, int BN, bool FP8, bool FP16>
-__global__ void __launch_bounds__(SplitShape<CG, BN>::kThreads, 1)
+__global__ void __launch_bounds__(kMatrixThreads, 1)
 linear_gate_split(const __grid_constant__ LinearParams p, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w) {
   using Shape = SplitShape<CG, BN>;
   extern __shared__ unsigned char raw[];
