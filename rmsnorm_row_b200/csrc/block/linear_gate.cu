@@ -126,23 +126,23 @@ fn_status launch_tokens(const linear_gate_s* h, LinearParams& p, cudaStream_t st
 // ---- many rows --------------------------------------------------------------------------------
 
 struct Variant {
-  int cg, mh, bn, shared, stages, received[9];  // received: bytes of sums by the parts of K, of a split tile
+  int cg, bn, shared, stages, received[9];  // received: bytes of sums by the parts of K, of a split tile
   void* kernel[3];  // by dtype: bf16, fp16, e4m3
-  int rows() const { return kTileM * cg * mh; }
+  int rows() const { return kTileM * cg; }
 };
-template <int CG, int MH, int BN>
+template <int CG, int BN>
 Variant variant() {
-  return Variant{CG, MH, BN, MatrixShape<CG, MH, BN>::kShared, MatrixShape<CG, MH, BN>::kStages, {},
-                 {(void*)linear_gate_tiles<CG, MH, BN, false, false>, (void*)linear_gate_tiles<CG, MH, BN, false, true>,
-                  MH == 2 ? nullptr : (void*)linear_gate_tiles<CG, 1, BN, true, false>}};
+  using S = MatrixShape<CG, BN>;
+  return Variant{CG, BN, S::kShared, S::kStages, {},
+                 {(void*)linear_gate_tiles<CG, BN, false, false>, (void*)linear_gate_tiles<CG, BN, false, true>,
+                  (void*)linear_gate_tiles<CG, BN, true, false>}};
 }
-const Variant kVariants[] = {variant<2, 2, 256>(), variant<2, 1, 256>(), variant<2, 1, 192>(), variant<2, 1, 128>(),
-                             variant<1, 1, 256>(), variant<1, 1, 128>(), variant<1, 1, 64>()};
+const Variant kVariants[] = {variant<2, 256>(), variant<2, 192>(), variant<2, 128>(), variant<1, 256>(), variant<1, 128>(), variant<1, 64>()};
 
 template <int CG, int BN>
 Variant split_variant() {
   using S = SplitShape<CG, BN>;
-  Variant v{CG, 1, BN, S::kShared, S::kStages, {},
+  Variant v{CG, BN, S::kShared, S::kStages, {},
             {(void*)linear_gate_split<CG, BN, false, false>, (void*)linear_gate_split<CG, BN, false, true>,
              (void*)linear_gate_split<CG, BN, true, false>}};
   for (int n = 1; n <= 8; ++n) v.received[n] = S::received(n);
@@ -155,15 +155,15 @@ const Variant kSplitVariants[] = {split_variant<2, 256>(), split_variant<1, 128>
 // 2064 14.9, 2056 19.1); and no step is shorter than its share of a load's 2500 cycles (16 x 5120
 // x 5120 as 80 CTAs of 8 stages: 335 cycles a step).
 int64_t step_cycles(const Variant& v, int64_t rows, int64_t row_bytes) {
-  const int64_t products = 2 * v.mh * v.bn;
-  const int64_t x = rows < kTileM * v.mh ? rows : kTileM * v.mh;  // rows past the last are not read
+  const int64_t products = 2 * v.bn;
+  const int64_t x = rows < kTileM ? rows : kTileM;  // rows past the last are not read
   const int percent = row_bytes % 128 == 0 ? 100 : row_bytes % 64 == 0 ? 120 : row_bytes % 32 == 0 ? 140 : 200;
   const int64_t bytes = (x + v.bn / v.cg) * kStepBytes * percent / 8000;
   const int64_t least = 2500 / v.stages, most = products > bytes ? products : bytes;
   return most > least ? most : least;
 }
 // What a tile takes besides: its way through the epilogue, which the next tile hides or not.
-int64_t drain_cycles(const Variant& v) { return 1500 + v.bn * v.mh * 16; }
+int64_t drain_cycles(const Variant& v) { return 1500 + v.bn * 16; }
 
 // A matrix of `rows` rows of `width` elements per batch, as a tensor map of boxes.
 struct Matrix {
@@ -235,15 +235,9 @@ fn_status launch_tiles(const linear_gate_s* h, const lg_args* a, LinearParams& p
   const Variant* best = nullptr;
   int64_t best_cost = 0, parts = 1;
   for (const Variant& v : kVariants) {
-    // The sums of a 512-row tile fill TMEM, so its epilogue costs some 7000 cycles that two tiles
-    // in turn hide. Over 80 steps of 16-bit operands the power saved is worth more (176400 x 5120 x
-    // 5120 sustained: 7.94 against 8.27 ms); over 40 steps of e4m3 it is not (4.43 against 3.98 ms).
-    if (v.mh == 2 && (c.dtype == BO_E4M3 || steps < 64)) continue;
     const int64_t tm = (rows + v.rows() - 1) / v.rows() * batches, tn = (c.N + v.bn - 1) / v.bn;
     const int64_t waves = (tm * tn + sms / v.cg - 1) / (sms / v.cg);
-    int64_t cost = waves * steps * step_cycles(v, rows, row_bytes);
-    if (v.mh == 2) cost -= cost / 32;
-    cost += drain_cycles(v);
+    const int64_t cost = waves * steps * step_cycles(v, rows, row_bytes) + drain_cycles(v);
     if (!best || cost < best_cost) best = &v, best_cost = cost;
   }
   // Few tiles: K split over a cluster, where its CTAs all run at once. Exchanging the sums takes
@@ -277,7 +271,7 @@ fn_status launch_tiles(const linear_gate_s* h, const lg_args* a, LinearParams& p
 
   const int out_type = c.dtype == BO_FP16 ? BO_FP16 : BO_BF16, per_step = kStepBytes / size;
   CUtensorMap mx, mw, mo = {}, mr;
-  fn_status s = encode(&mx, c.dtype, matrix(a->x.ptr, c.K, a->x.stride_b, a->x.stride_l), per_step, kTileM * v.mh, CU_TENSOR_MAP_SWIZZLE_128B);
+  fn_status s = encode(&mx, c.dtype, matrix(a->x.ptr, c.K, a->x.stride_b, a->x.stride_l), per_step, kTileM, CU_TENSOR_MAP_SWIZZLE_128B);
   if (s == FN_OK)
     s = encode(&mw, c.dtype, Matrix{a->weight, c.K, c.N, a->weight_stride, 1, 0}, per_step, v.bn / v.cg, CU_TENSOR_MAP_SWIZZLE_128B);
   if (s == FN_OK && parts == 1)

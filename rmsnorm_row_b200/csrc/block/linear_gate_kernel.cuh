@@ -6,14 +6,15 @@
 //
 // Many rows: persistent CTAs or CTA pairs (CG = 2) of ten warps. One thread loads 128-byte
 // wide tiles of x and W by TMA into a ring of shared-memory stages, one thread issues the
-// tcgen05 products of a 128 MH CG x BN tile into TMEM, eight warps read the sums back, a row per
-// thread, and finish them. A pair shares W's tile: each CTA loads half of it. TMEM holds two
-// blocks of sums, so that the epilogue of one runs under the products of the other: two tiles in
-// turn (MH = 1), or two blocks of rows of one tile (MH = 2), which read W once. Large problems
-// are bound by the power that the chip may draw, and the operands' way from L2 takes its share:
-// a 512 x 256 tile moves a quarter less than a 256 x 256 one. Residual and output pass through
-// shared memory in boxes of 32 x 32: TMA brings a warp's next residual box while the present
-// one is worked on in place, and stores it.
+// tcgen05 products of a 128 CG x BN tile into TMEM, eight warps read the sums back, a row per
+// thread, and finish them. TMEM holds two tiles, so the epilogue of one runs under the products
+// of the next. A pair shares W's tile: each CTA loads half of it. Residual and output pass
+// through shared memory in boxes of 32 x 32: TMA brings a warp's next residual box while the
+// present one is worked on in place, and stores it. The tensor pipe is 95% busy at 18944 x 5120 x
+// 5120; over seconds the power that the chip may draw sets the clock instead (176400 rows with
+// residual: 6.3 ms at first, 7.2 to 8.0 sustained at 1.0 to 1.1 GHz; cuBLAS without epilogue 5.7
+// and 6.6). Tiles of 512 x 256 move a quarter less through L2 but leave TMEM no second tile: 7.4
+// against 7.2 ms.
 //
 // A few tokens: every warp streams rows of W past the tokens with 16-byte loads.
 #pragma once
@@ -176,12 +177,12 @@ constexpr int kMatrixThreads = 32 * (2 + kEpilogueWarps);
 constexpr int kBox = 32;             // rows and columns of an output box
 constexpr int kBoxBytes = kBox * kBox * 2;
 
-// CG CTAs work on a tile together, each on MH blocks of kTileM rows and all BN columns of it.
-template <int CG, int MH, int BN>
+// CG CTAs work on a tile together, each on kTileM rows and all BN columns of it.
+template <int CG, int BN>
 struct MatrixShape {
-  static constexpr int kABytes = MH * kTileM * kStepBytes, kBBytes = BN / CG * kStepBytes;
+  static constexpr int kABytes = kTileM * kStepBytes, kBBytes = BN / CG * kStepBytes;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kBoxes = MH == 2 ? 2 : 4;  // of a warp: half of them being brought, one worked on, the rest being stored
+  static constexpr int kBoxes = 4;  // of a warp: two being brought, one worked on, one being stored
   static constexpr int kBoxesBytes = kEpilogueWarps * kBoxes * kBoxBytes;
   static constexpr int kFit = (226 * 1024 - 1024 - kBoxesBytes) / kStageBytes;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
@@ -205,12 +206,12 @@ __device__ __forceinline__ Tile tile_at(const LinearParams& p, uint32_t t) {
 
 __device__ int linear_gate_gave_up = 0;  // launches in which a wait ran out (this file is included once)
 
-template <int CG, int MH, int BN, bool FP8, bool FP16>
+template <int CG, int BN, bool FP8, bool FP16>
 __global__ void __launch_bounds__(kMatrixThreads, 1)
 linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant__ CUtensorMap map_x,
                   const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_out,
                   const __grid_constant__ CUtensorMap map_residual) {
-  using S = MatrixShape<CG, MH, BN>;
+  using S = MatrixShape<CG, BN>;
   constexpr int kBoxes = S::kBoxes, kAhead = kBoxes / 2;
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], sums_full[2], sums_empty[2];
@@ -248,7 +249,7 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
       bool ok = true;
       for (uint32_t t = first; ok && t < p.tiles; t += step) {
         const Tile at = tile_at(p, t);
-        const int row = (int)((at.m * CG + rank) * MH * kTileM), col = (int)(at.n * BN + rank * (BN / CG));
+        const int row = (int)((at.m * CG + rank) * kTileM), col = (int)(at.n * BN + rank * (BN / CG));
         for (uint32_t k = 0; k < p.steps; ++k) {
           if (!(ok = mbar_wait(smem_u32(&empty[stage]), parity ^ 1, &failed))) break;
           uint32_t bar = smem_u32(&full[stage]);
@@ -270,59 +271,22 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
     if (rank == 0 && elect_one()) {
       uint32_t stage = 0, parity = 0, n = 0;
       bool ok = true;
-      // The products of block `half` with stage s into its sums.
-      auto multiply = [&](uint32_t s, uint32_t acc, int half, bool add) {
-        const uint32_t a = stages + s * S::kStageBytes;
-        const uint64_t da = operand_desc(a + half * kTileM * kStepBytes), db = operand_desc(a + S::kABytes);
-#pragma unroll
-        for (int i = 0; i < kStepBytes / 32; ++i)  // 32 bytes of K each
-          mma<CG, FP8>(tmem + acc * BN, da + 2 * i, db + 2 * i, p.idesc, add || i > 0);
-      };
-      auto wait_full = [&](uint32_t s, uint32_t par) {
-        const bool got = mbar_wait(smem_u32(&full[s]), par, &failed);
+      for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
+        const uint32_t buf = n & 1, round = (n >> 1) & 1;
+        if (!(ok = mbar_wait(smem_u32(&sums_empty[buf]), round ^ 1, &failed))) break;
         tc_fence_after();
-        return got;
-      };
-      if (MH == 1) {
-        for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
-          const uint32_t buf = n & 1, round = (n >> 1) & 1;
-          if (!(ok = mbar_wait(smem_u32(&sums_empty[buf]), round ^ 1, &failed))) break;
+        for (uint32_t k = 0; k < p.steps; ++k) {
+          if (!(ok = mbar_wait(smem_u32(&full[stage]), parity, &failed))) break;
           tc_fence_after();
-          for (uint32_t k = 0; k < p.steps; ++k) {
-            if (!(ok = wait_full(stage, parity))) break;
-            multiply(stage, buf, 0, k > 0);
-            mma_commit<CG>(smem_u32(&empty[stage]));
-            if (++stage == S::kStages) stage = 0, parity ^= 1;
-          }
-          if (ok) mma_commit<CG>(smem_u32(&sums_full[buf]));
+          const uint32_t a = stages + stage * S::kStageBytes;
+          const uint64_t da = operand_desc(a), db = operand_desc(a + S::kABytes);
+#pragma unroll
+          for (int i = 0; i < kStepBytes / 32; ++i)  // 32 bytes of K each
+            mma<CG, FP8>(tmem + buf * BN, da + 2 * i, db + 2 * i, p.idesc, k > 0 || i > 0);
+          mma_commit<CG>(smem_u32(&empty[stage]));
+          if (++stage == S::kStages) stage = 0, parity ^= 1;
         }
-      } else {
-        // Runs of stages, first block 0 and then block 1: long ones at a tile's ends, so that the
-        // sums of one block are read out while the other's products run; a stage elsewhere.
-        const uint32_t most = S::kStages - 1, ends = p.steps / 2 < most ? p.steps / 2 : most;
-        for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
-          for (uint32_t k = 0, run; ok && k < p.steps; k += run) {
-            run = (k == 0 || k + ends == p.steps) && ends > 1 ? ends : 1;
-            const bool last = k + run == p.steps;
-            uint32_t s = stage, par = parity;
-            if (k == 0) ok = mbar_wait(smem_u32(&sums_empty[0]), (n & 1) ^ 1, &failed);
-            for (uint32_t i = 0; ok && i < run; ++i) {
-              if (!(ok = wait_full(s, par))) break;
-              multiply(s, 0, 0, k + i > 0);
-              if (++s == S::kStages) s = 0, par ^= 1;
-            }
-            if (ok && last) mma_commit<CG>(smem_u32(&sums_full[0]));
-            if (ok && k == 0) ok = mbar_wait(smem_u32(&sums_empty[1]), (n & 1) ^ 1, &failed);
-            if (!ok) break;
-            tc_fence_after();
-            for (uint32_t i = 0; i < run; ++i) {
-              multiply(stage, 1, 1, k + i > 0);
-              mma_commit<CG>(smem_u32(&empty[stage]));
-              if (++stage == S::kStages) stage = 0, parity ^= 1;
-            }
-            if (last) mma_commit<CG>(smem_u32(&sums_full[1]));
-          }
-        }
+        if (ok) mma_commit<CG>(smem_u32(&sums_full[buf]));
       }
     }
   } else {
@@ -332,30 +296,28 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
     const uint32_t boxes = stages + S::kStages * S::kStageBytes + mine * kBoxes * kBoxBytes;
     const uint32_t bars = smem_u32(&box_full[mine][0]);
     // The residual boxes of this warp's chunks, brought in order, kAhead ahead; lane 0 only.
-    uint32_t next_t = first, next_c = 0, next_box = 0;  // next_c: over the chunks of the tile's blocks
-    auto row_of = [&](const Tile& at, uint32_t half) { return ((at.m * CG + rank) * MH + half) * kTileM + quarter * 32; };
+    uint32_t next_t = first, next_c = 0, next_box = 0;
+    auto row_of = [&](const Tile& at) { return (at.m * CG + rank) * kTileM + quarter * 32; };
     auto fetch = [&]() {
       if (next_t >= p.tiles) return;
       const Tile at = tile_at(p, next_t);
       mbar_expect(bars + 8 * next_box, kBoxBytes);
-      tma_load<false>(boxes + next_box * kBoxBytes, &map_residual, (int)(at.n * BN + half + next_c % kChunks * kBox),
-                      (int)row_of(at, next_c / kChunks), (int)at.batch, bars + 8 * next_box);
+      tma_load<false>(boxes + next_box * kBoxBytes, &map_residual, (int)(at.n * BN + half + next_c * kBox),
+                      (int)row_of(at), (int)at.batch, bars + 8 * next_box);
       next_box = (next_box + 1) % kBoxes;
-      if (++next_c == MH * kChunks) next_c = 0, next_t += step;
+      if (++next_c == kChunks) next_c = 0, next_t += step;
     };
     if (p.has_residual && lane == 0)
       for (int i = 0; i < kAhead; ++i) fetch();
-    uint32_t chunk = 0;
+    uint32_t n = 0, chunk = 0;
     bool ok = true;
-    for (uint32_t n = 0;; ++n) {  // blocks of rows: MH to a tile
-      const uint32_t t = first + n / MH * step;
-      if (!ok || t >= p.tiles) break;
+    for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
       const uint32_t acc = n & 1, round = (n >> 1) & 1;
       if (!(ok = mbar_wait(smem_u32(&sums_full[acc]), round, &failed))) break;
       __syncwarp();
       tc_fence_after();
       const Tile at = tile_at(p, t);
-      const uint32_t row0 = row_of(at, n % MH);
+      const uint32_t row0 = row_of(at);
       const bool live = row0 + lane < p.batch_rows;
       const RowOut r = row_out(p, live ? at.batch * p.batch_rows + row0 + lane : 0u);
       const uint32_t n0 = at.n * BN + half;

@@ -148,7 +148,8 @@ def test_against_the_formula(case):
 
 
 # Few tiles, where K is split over a cluster: two to eight parts, pairs of CTAs, parts that own one
-# chunk of columns or none, K that does not divide; rows of batches apart. And a 512-row tile.
+# chunk of columns or none, K that does not divide; rows of batches apart. And the sizes between,
+# which take pairs of CTAs on 192 or 128 columns.
 SPLIT = [
     (1, 999, 2056, 1288, HF, 0, "silu", True, "none", False),
     (3, 333, 2056, 1288, BF, 0, "none", True, "batch", True),
@@ -163,12 +164,16 @@ SPLIT = [
     (1, 1500, 3000, 1000, BF, 0, "gelu_tanh", True, "none", True),
     (1, 9, 520, 520, HF, 0, "none", True, "none", False),
     (1, 37800, 4096, 512, BF, 21, "silu", True, "frame", True),
+    (1, 1024, 1024, 5120, BF, 0, "none", True, "row", True),
+    (1, 512, 5120, 5120, F8, 0, "silu", True, "none", True),
+    (5, 420, 1000, 2504, HF, 21, "gelu", True, "frame", True),
+    (1, 4096, 1536, 1544, BF, 0, "none", False, "bcast", True),
     (1, 37800, 4104, 520, HF, 0, "none", False, "none", False),
 ]
 
 
 @pytest.mark.parametrize("case", SPLIT, ids=lambda c: "-".join(str(v).replace("torch.", "") for v in c))
-def test_split_sums_and_long_tiles(case):
+def test_split_sums_and_pairs(case):
     B, L, K, N, dtype, F, act, bias, gate, residual = case
     before = timeouts()
     t = make(B, L, K, N, dtype, F, bias, gate, residual, seed=300)
