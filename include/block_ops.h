@@ -54,7 +54,8 @@ typedef enum { BO_BF16 = 0, BO_FP16 = 1, BO_E4M3 = 2, BO_FP32 = 3 } bo_dtype;
  * taken again in fp64). q is rounded once to nearest even. A row with a = 0 has row_scale 1;
  * a below 2^-100 is taken as 2^-100. A NaN or infinity in y leaves a NaN or infinite
  * row_scale: q is then NaN where y was not finite, and NaN everywhere in a NaN row.
- * 1 / sqrt(variance + eps) has to be below 2^127 (it is for any eps >= 2^-250).
+ * 1 / sqrt(variance + eps) has to be below 2^127 (it is for any eps >= 2^-250), and
+ * weight (1 + scale) and bias (1 + scale) + shift, which are formed first, within fp32.
  */
 typedef struct norm_quant_s* norm_quant_t;
 
@@ -174,7 +175,8 @@ fn_status rope_norm_destroy(rope_norm_t h);
  *
  * x and W are both bf16, both fp16 or both e4m3 (then x W^T is x_scale[row] * weight_scale[n]
  * times the product of the codes, and bias, gate, residual and out are bf16; otherwise they
- * have x's type). The sum over K and everything after it is fp32; out is rounded once.
+ * have x's type). The sum over K and everything after it is fp32; out is rounded once. The
+ * order of the sum depends on the sizes, not on the run.
  * act is SiLU z / (1 + e^-z), GELU z Phi(z), its tanh form, or nothing.
  */
 typedef struct linear_gate_s* linear_gate_t;

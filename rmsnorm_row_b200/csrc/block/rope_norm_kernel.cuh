@@ -17,6 +17,9 @@
 // Half pairing puts the 8 partners of A in B, so every pair is inside one thread; adjacent
 // pairing has A in the head's first half and B in its second, so that neighbouring lanes touch
 // neighbouring vectors. A norm over the head is a shuffle inside W lanes.
+//
+// B200, 40 heads of 128: 176400 tokens forward 639 us, 5.7 TB/s of the 6.6 of a plain copy (1730
+// instructions a row); gradient of 90000 tokens 588 us, 4.7 TB/s (4100 a row, issue 58% busy).
 #pragma once
 
 #include "../../../include/block_ops.h"
@@ -512,9 +515,9 @@ __device__ __forceinline__ void copy_async(uint4* to, const uint16_t* from, uint
 }
 
 // Shared memory of a CTA: the frequency table, sums; then three tables of cos and sin per row
-// slot, the weights, and the stages of rows (two, or one where two do not fit). A row's table is written before the barrier of the row
-// ahead of it and read up to the barrier of the row behind it, so its buffer comes round again
-// at the third row.
+// slot, the weights, and the stages of rows (two, or one where two do not fit). A row's table is
+// written before the barrier of the row ahead of it and read up to the barrier of the row behind
+// it, so its buffer comes round again at the third row.
 constexpr int kTables = 3;
 struct alignas(16) BackwardShared {
   double turns[kMaxPairs];
