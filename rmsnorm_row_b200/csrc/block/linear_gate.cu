@@ -104,21 +104,28 @@ LinearParams make_params(const linear_gate_s* h, const lg_args* a) {
 
 // ---- a few tokens ---------------------------------------------------------------------------
 
-template <bool FP8, bool FP16>
+template <int PARTS, bool FP8, bool FP16>
 void* token_kernel(int M) {
   switch (M) {
-    case 1: return (void*)linear_gate_tokens<1, FP8, FP16>;
-    case 2: return (void*)linear_gate_tokens<2, FP8, FP16>;
-    case 3: return (void*)linear_gate_tokens<3, FP8, FP16>;
-    default: return (void*)linear_gate_tokens<4, FP8, FP16>;
+    case 1: return (void*)linear_gate_tokens<1, PARTS, FP8, FP16>;
+    case 2: return (void*)linear_gate_tokens<2, PARTS, FP8, FP16>;
+    case 3: return (void*)linear_gate_tokens<3, PARTS, FP8, FP16>;
+    default: return (void*)linear_gate_tokens<4, PARTS, FP8, FP16>;
   }
 }
+template <int PARTS>
+void* token_kernel(int dtype, int M) {
+  return dtype == BO_E4M3 ? token_kernel<PARTS, true, false>(M) : dtype == BO_FP16 ? token_kernel<PARTS, false, true>(M) : token_kernel<PARTS, false, false>(M);
+}
+
+// Four warps share K, except for three and four tokens where N keeps the GPU busy with a warp to
+// its columns (four tokens, 5120 -> 30720 65.5 against 70.7 us, -> 5120 20.5 against 15.0; one
+// token, -> 30720 52.4 against 48.0, -> 5120 16.5 against 10.2).
+constexpr uint32_t kBusyColumns = 16384;
 
 fn_status launch_tokens(const linear_gate_s* h, LinearParams& p, cudaStream_t stream) {
-  const int per_cta = kTokenThreads / 32 * kTokenColumns;
-  void* kernel = h->cfg.dtype == BO_E4M3   ? token_kernel<true, false>(p.rows)
-                 : h->cfg.dtype == BO_FP16 ? token_kernel<false, true>(p.rows)
-                                           : token_kernel<false, false>(p.rows);
+  const int parts = p.rows > 2 && p.N >= kBusyColumns ? 1 : 4, per_cta = kTokenThreads / 32 / parts * kTokenColumns;
+  void* kernel = parts == 1 ? token_kernel<1>(h->cfg.dtype, p.rows) : token_kernel<4>(h->cfg.dtype, p.rows);
   void* args[] = {&p};
   return launch_status(cudaLaunchKernel(kernel, dim3((p.N + per_cta - 1) / per_cta), dim3(kTokenThreads), args, 0, stream));
 }

@@ -168,6 +168,14 @@ SPLIT = [
     (1, 512, 5120, 5120, F8, 0, "silu", True, "none", True),
     (5, 420, 1000, 2504, HF, 21, "gelu", True, "frame", True),
     (1, 4096, 1536, 1544, BF, 0, "none", False, "bcast", True),
+    # a few tokens: a warp or four to the columns, K shorter than their reach, columns that end inside a CTA
+    (1, 4, 520, 16392, BF, 0, "silu", True, "row", True),
+    (3, 1, 1040, 16384, F8, 0, "none", True, "batch", True),
+    (1, 3, 1032, 16384, HF, 0, "gelu", True, "bcast", True),
+    (1, 2, 13824, 520, HF, 2, "gelu_tanh", True, "frame", True),
+    (1, 4, 4104, 8, BF, 0, "none", True, "none", True),
+    (1, 1, 16, 24, F8, 0, "none", True, "none", False),
+    (2, 1, 264, 30728, BF, 0, "none", False, "vec", True),
     (1, 37800, 4104, 520, HF, 0, "none", False, "none", False),
 ]
 
