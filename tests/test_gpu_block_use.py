@@ -147,3 +147,27 @@ def test_refusals():
         fn.rope_norm(q, pos, (16, 16), rand(64), norm="all")
     with pytest.raises(ValueError, match="on cpu"):
         fn.rope_norm(q, pos.cpu(), (16, 16))
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^32 elements: the last rows are those of a call on them alone."""
+    L, D = 270000, 16384
+    tail = slice(L - 70, L)
+    x, w = rand(1, 1, D).expand(1, L, D).contiguous(), rand(D, seed=1)
+    x[:, tail] = rand(1, 70, D, seed=2)
+    q, s = fn.norm_scale_shift_quant(x, w, None, None, None, "rms")
+    q2, s2 = fn.norm_scale_shift_quant(x[:, tail], w, None, None, None, "rms")
+    assert same((q[:, tail], s[:, tail]), (q2, s2)) and torch.all(s[:, :-70] == s[0, 0])
+    del q, s
+    heads, pos = x.view(1, L, 128, 128), torch.arange(L, device="cuda", dtype=torch.int32)[:, None]
+    want = fn.rope_norm(heads[:, tail], pos[tail], (64,), w)
+    back = fn.rope_norm_backward(heads[:, tail], heads[:, tail], pos[tail], (64,), w)[0]
+    got = fn.rope_norm_backward(heads, heads, pos, (64,), w)[0]
+    assert same(got[:, tail], back)
+    del got
+    assert same(fn.rope_norm(heads, pos, (64,), w, out=heads)[:, tail], want)
+    small, weight = rand(1, L, 64), rand(D, 64, seed=3)
+    out = fn.linear_gate_residual(small, weight, residual=x, out=x)
+    again = fn.linear_gate_residual(small[:, tail], weight, residual=want.view(1, 70, D))
+    # one step of K in both: the same sums, whatever the tiles
+    assert same(out[:, tail], again)
