@@ -549,6 +549,10 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_norm_gradient(const __gr
   float* const weights = tables + (size_t)kTables * R * p.hd;
   uint4* const stages = reinterpret_cast<uint4*>(weights + weight_floats(p.weight_units)) + threadIdx.x;
   for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) sh.turns[i] = p.turns[i], sh.axis[i] = p.axis[i];
+  // A slot without a row turns its zeros by what its table holds, and they are added to dweight:
+  // what another kernel left there may be a NaN.
+  if (!wide)
+    for (int i = threadIdx.x; i < kTables * R * p.hd; i += blockDim.x) tables[i] = 0.0f;
   fill_weights<FP16, HALF>(p, weights);
   __syncthreads();
   const int apart = q.offB - q.offA;

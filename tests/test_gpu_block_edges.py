@@ -1,0 +1,48 @@
+"""GPU tests of the operators of include/block_ops.h at the edges of their calls: row slots
+without a row, long sums, rare values, calls from several host threads, autograd."""
+import pytest
+import torch
+
+import rmsnorm_row_b200 as fn
+
+pytestmark = pytest.mark.gpu
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def rand(*shape, seed=0, dtype=BF, sd=1.0, mean=0.0):
+    g = torch.Generator(device="cuda").manual_seed(seed + sum(shape))
+    return torch.empty(shape, device="cuda").normal_(mean, sd, generator=g).to(dtype)
+
+
+def leave_nan_in_shared_memory():
+    """Rows of 1024 heads keep their 16384 weights in shared memory, here NaN."""
+    x = rand(1, 2000, 1024, 16)
+    pos = torch.zeros(2000, 1, device="cuda", dtype=torch.int32)
+    y = fn.rope_norm(x, pos, (8,), torch.full((16384,), float("nan"), device="cuda"))
+    assert torch.isnan(y).all()
+
+
+@pytest.mark.parametrize("norm", ["head", "all"])
+@pytest.mark.parametrize("H,hd,L", [(1, 16, 5), (1, 16, 200), (2, 16, 300), (1, 64, 3), (4, 128, 9), (3, 48, 1)])
+def test_slots_without_a_row_add_nothing_to_dweight(H, hd, L, norm):
+    """Several rows share a CTA; what shared memory holds where it has none does not count.
+
+    dweight is a sum of L H (or L) terms dn x rho, each within 40 u of (|g0| + |g1|) |x| rho, in
+    chains of at most L H: (40 + L H) u of the terms' magnitudes."""
+    x, g = rand(1, L, H, hd), rand(1, L, H, hd, seed=1)
+    w = rand(hd if norm == "head" else H * hd, seed=2)
+    pos = torch.arange(L, device="cuda", dtype=torch.int32)[:, None]
+    leave_nan_in_shared_memory()
+    dx, dw = fn.rope_norm_backward(g, x, pos, (hd // 2,), w, norm=norm)
+    x64 = x.double()
+    dims = (-1,) if norm == "head" else (-2, -1)
+    n = x64 / (x64.square().mean(dims, keepdim=True) + 1e-6).sqrt()
+    i = torch.arange(hd // 2, device="cuda", dtype=torch.float64)
+    a = (pos.double() * 10000.0 ** (-i / (hd // 2)))[None, :, None, :]
+    g0, g1 = g.double()[..., 0::2], g.double()[..., 1::2]
+    dn = torch.stack((g0 * a.cos() + g1 * a.sin(), g1 * a.cos() - g0 * a.sin()), -1).flatten(-2)
+    size = (g0.abs() + g1.abs()).repeat_interleave(2, -1)
+    over = (0, 1, 2) if norm == "head" else (0, 1)
+    want, bound = (dn * n).sum(over).flatten(), (size * n.abs()).sum(over).flatten()
+    assert torch.all((dw.double() - want).abs() <= (40 + L * H) * 2.0 ** -24 * bound)
+    assert not torch.isnan(dx).any()
