@@ -84,12 +84,14 @@ __device__ __forceinline__ void load_affine(const void* p, bool fp32, int j, uin
   }
 }
 
-// y = n a + b of a vector: a = weight (1 + scale), b = bias (1 + scale) + shift.
+// y = n a + b of a vector: a = weight (1 + scale), b = bias (1 + scale) + shift. Where there is
+// neither bias nor modulation b is -0, which leaves every n a as it is, a zero's sign too: the
+// kernels that have no b give the same.
 __device__ __forceinline__ void coefficients(const QuantParams& p, int j, bool modulated, const uint4& scale, const uint4& shift,
                                              uint64_t (&a)[4], uint64_t (&b)[4]) {
   const uint64_t one = pk2(1.0f, 1.0f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] = one, b[i] = 0;
+  for (int i = 0; i < 4; ++i) a[i] = one, b[i] = modulated ? 0 : pk2(-0.0f, -0.0f);
   if (p.weight) load_affine(p.weight, p.affine_fp32, j, a);
   if (p.bias) load_affine(p.bias, p.affine_fp32, j, b);
   if (modulated) {

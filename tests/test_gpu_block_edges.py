@@ -46,3 +46,39 @@ def test_slots_without_a_row_add_nothing_to_dweight(H, hd, L, norm):
     want, bound = (dn * n).sum(over).flatten(), (size * n.abs()).sum(over).flatten()
     assert torch.all((dw.double() - want).abs() <= (40 + L * H) * 2.0 ** -24 * bound)
     assert not torch.isnan(dx).any()
+
+
+# ---- norm_quant --------------------------------------------------------------------------------
+
+def codes(q):
+    return q.view(torch.uint8)
+
+
+@pytest.mark.parametrize("norm", ["layer", "rms"])
+@pytest.mark.parametrize("D,affine,mod", [(512, BF, False), (5120, BF, False), (5120, F32, True), (512, None, True), (512, None, False)])
+def test_zeros_keep_their_sign_in_one_row_and_in_many(D, affine, mod, norm):
+    """Many rows and the same rows a few at a time give the same bytes, zeros' signs included;
+    without bias and modulation a zero's sign is that of n w."""
+    rows = 4000
+    x = rand(1, rows, D)
+    x[:, :, ::7] = -0.0
+    w = None
+    if affine is not None:
+        w = rand(D, seed=1, dtype=affine)
+        w[::5] = 0.0
+        w[1::5] = -0.0
+    sc = sh = None
+    if mod:
+        sc, sh = rand(D, seed=2), rand(D, seed=3)
+        sh[::3] = -0.0
+        sh[1::3] = 0.0
+    q, s = fn.norm_scale_shift_quant(x, w, None, sc, sh, norm)
+    for at in range(0, rows, 1000):
+        part = slice(at, at + 3)
+        q1, s1 = fn.norm_scale_shift_quant(x[:, part], w, None, sc, sh, norm)
+        assert torch.equal(codes(q1), codes(q[:, part])) and torch.equal(s1, s[:, part])
+    if norm == "rms" and not mod:
+        y = x.double() * (1.0 if w is None else w.double())
+        zero = y == 0
+        assert zero.any() and torch.equal(codes(q)[zero] == 0x80, torch.signbit(y)[zero])
+
