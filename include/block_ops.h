@@ -109,7 +109,9 @@ fn_status norm_quant_destroy(norm_quant_t h);
  *
  * The gradient, of the same handle: with dn the grad turned back,
  *   dx = rho (w dn - x rho^2 mean(w dn x)),  dweight = sum over tokens (and heads, for
- * BO_NORM_HEAD) of dn x rho, in fp32 per thread and fp64 across threads, in a fixed order.
+ * BO_NORM_HEAD) of dn x rho, in a fixed order: in fp32 over runs of at most 512 tokens of a thread
+ * (up to 4 heads of each for BO_NORM_HEAD, so an error of at most 2048 2^-24 of the terms'
+ * magnitudes), in fp64 across threads; a CTA's runs are added in fp32.
  */
 typedef struct rope_norm_s* rope_norm_t;
 
@@ -165,7 +167,8 @@ fn_status rope_norm_launch(rope_norm_t h, const rn_args* a, fn_stream_t stream);
 /* Bytes of workspace for a backward launch over B * L tokens, on any device. */
 fn_status rope_norm_backward_workspace(rope_norm_t h, int64_t B, int64_t L, uint64_t* bytes);
 fn_status rope_norm_backward_validate(rope_norm_t h, const rn_backward_args* a);
-/* One kernel launch, and a second one that sums dweight. */
+/* One kernel launch (with a weight, one for every 512 tokens of each of its threads), and one that
+ * sums dweight. */
 fn_status rope_norm_backward_launch(rope_norm_t h, const rn_backward_args* a, fn_stream_t stream);
 fn_status rope_norm_destroy(rope_norm_t h);
 

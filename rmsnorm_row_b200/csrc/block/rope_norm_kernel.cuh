@@ -32,6 +32,7 @@ constexpr int kRopeThreads = 512;   // of a CTA, at most
 constexpr int kForwardThreads = 384;  // of a forward CTA: 168 registers hold a lane's ten heads
 constexpr int kSharedRows = 128;    // threads of a CTA whose rows take 32 lanes or fewer
 constexpr int kMaxPartials = 1024;  // CTAs that sum dweight
+constexpr int kMaxTurns = 512;      // rows (of each slot) that a CTA sums dweight over in a launch
 
 struct RopeRows {
   const uint16_t* ptr;
@@ -45,7 +46,9 @@ struct RopeParams {
   int64_t pos_sb, pos_sl;
   const void* weight;
   float* partial;
-  uint32_t rows, L;
+  uint32_t rows, L;         // rows up to which the launch goes
+  uint32_t first;           // the gradient: its first row
+  int add;                  // the CTAs' parts of dweight are added to those of a launch before
   DivU32 div_L;
   int H, hd, units, pairs;  // units of a head (hd / 16), pairs that turn
   int W, T, G;              // lanes of a head, threads of a row, lane groups (of a warp, in the forward kernel)
@@ -627,7 +630,7 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_norm_gradient(const __gr
   auto outside = [](float xx, float gx) { return !(in_range(xx) && fabsf(gx) <= 0x1p+100f); };
 
   const uint32_t step = gridDim.x * R;
-  uint32_t base = blockIdx.x * R;
+  uint32_t base = p.first + blockIdx.x * R;
   RowAt at = row_at(p, base + slot), at1 = row_at(p, base + slot + step);  // rows + 2 step < 2^32: the host bounds both
   if (p.stages > 1) fetch(at, base + slot < p.rows, 0);
   Angles angles{sh.turns, sh.axis, make_int2(0, 0)};
@@ -740,44 +743,39 @@ __global__ void __launch_bounds__(kRopeThreads, 1) rope_norm_gradient(const __gr
     upk2(acc[k][i / 2], v[0], v[1]);
     return v[i & 1];
   };
+  auto put = [&](const Place& at, int k, int i, float v) {
+    float& to = part[(NORM == BO_NORM_ALL ? (at.g + k * p.G) * p.hd : 0) + channel_of<HALF>(at, (i / 2) % 4, i & 1, i / 8)];
+    to = p.add ? to + v : v;
+  };
   if (NORM == BO_NORM_ALL && wide) {  // every channel of the token has one thread
 #pragma unroll
     for (int k = 0; k < NACC; ++k) {
       if (!has(k)) continue;
-      float* o = part + (q.g + k * p.G) * p.hd;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[channel_of<HALF>(q, (i / 2) % 4, i & 1, i / 8)] = value(k, i);
+      for (int i = 0; i < 16; ++i) put(q, k, i, value(k, i));
     }
     return;
   }
-  // Threads with the same channels: lanes of a warp through shuffles, then warps in turn,
-  // through the first stage (every thread is past its rows, and its copies have landed).
+  // Threads with the same channels, `span` apart, are summed in fp64 and in their order, from shared
+  // memory (the first stage: every thread is past its rows, and its copies have landed). Rolled: what
+  // the loops keep in registers here would set the allocation of the rows' loop.
   asm volatile("cp.async.wait_all;" ::: "memory");
-  const int span = NORM == BO_NORM_ALL ? T : p.W;
-  float* const sums = reinterpret_cast<float*>(stages - threadIdx.x);  // 16 values of `span` lanes
+  const int span = NORM == BO_NORM_ALL ? T : p.W, threads = blockDim.x;
+  float* const sums = reinterpret_cast<float*>(stages - threadIdx.x);
 #pragma unroll
   for (int k = 0; k < NACC; ++k) {
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      v[i] = value(k, i);
-      for (int o = span; o < 32; o <<= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
-    }
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-      __syncthreads();
-      if ((int)(threadIdx.x >> 5) == w && (int)(threadIdx.x & 31) < span) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float& s = sums[i * 32 + (threadIdx.x & 31)];
-          s = (w ? s : 0.0f) + v[i];
-        }
-      }
-    }
     __syncthreads();
-    if ((int)threadIdx.x < span && has(k)) {
-      float* o = part + (NORM == BO_NORM_ALL ? (q.g + k * p.G) * p.hd : 0);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[channel_of<HALF>(q, (i / 2) % 4, i & 1, i / 8)] = sums[i * 32 + threadIdx.x];
+    for (int i = 0; i < 16; ++i) sums[i * threads + threadIdx.x] = value(k, i);
+    __syncthreads();
+#pragma unroll 1
+    for (int j = threadIdx.x; j < 16 * span; j += threads) {
+      const int i = j / span;
+      const Place at = place_of<HALF>(p, j - i * span);
+      double s = 0.0;
+#pragma unroll 1
+      for (int from = j - i * span; from < threads; from += span) s += (double)sums[i * threads + from];
+      if (at.owns && at.g + k * p.G < p.H) put(at, k, i, (float)s);
     }
   }
 }

@@ -82,3 +82,39 @@ def test_zeros_keep_their_sign_in_one_row_and_in_many(D, affine, mod, norm):
         zero = y == 0
         assert zero.any() and torch.equal(codes(q)[zero] == 0x80, torch.signbit(y)[zero])
 
+
+# ---- long sums of dweight ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("H,hd,L,norm,step,terms", [(40, 128, 1800000, "all", 13, 1), (40, 128, 1800000, "head", 12, 2), (40, 128, 90000, "head", 12, 2),
+                                                    (2, 64, 3000000, "all", 13, 1), (1, 16, 5000000, "head", 13, 1), (24, 48, 300000, "head", 13, 4)])
+def test_dweight_of_many_tokens(H, hd, L, norm, step, terms):
+    """x and grad are 1, nothing turns, and eps makes every term rho = 1 - 1.1 * 2^-step: an fp32 sum
+    of 2^(step - 2) and more loses almost half of its last place with each term.
+
+    rho is off by 23 u. A thread sums 512 tokens of `terms` heads in fp32: 512 terms u; the runs of a
+    CTA are added in fp32, L / (512 * 444) of them at the least 148 * 3 CTAs: 8 u. Joining in fp64
+    and the roundings to fp32 add 3 u."""
+    rho = 1 - 1.1 * 2.0 ** -step
+    one = torch.ones(1, 1, 1, 1, device="cuda", dtype=BF).expand(1, 1, H, hd).contiguous().expand(1, L, H, hd)
+    w = torch.ones(hd if norm == "head" else H * hd, device="cuda", dtype=BF)
+    pos = torch.zeros(1, 1, device="cuda", dtype=torch.int32).expand(L, 1)
+    dw = fn.rope_norm_backward(one, one, pos, (hd // 2,), w, norm=norm, eps=rho ** -2 - 1)[1].double()
+    want = rho * L * (H if norm == "head" else 1)
+    assert (dw - want).abs().max().item() <= (23 + 512 * terms + 8 + 3) * 2.0 ** -24 * want
+
+
+def test_runs_of_dweight_add_up():
+    """Tokens beyond a launch's: dx is that of the tokens alone, dweight the sum over the parts."""
+    H, hd, L = 40, 128, 600000
+    x, g, w = rand(1, 1000, H, hd), rand(1, 1000, H, hd, seed=1), rand(H * hd, seed=2)
+    pos = torch.arange(1000, device="cuda", dtype=torch.int32)[:, None]
+    dx1, dw1 = fn.rope_norm_backward(g, x, pos, (hd // 2,), w)
+    again = lambda t: t.expand(L // 1000, *t.shape[1:])
+    dx, dw = fn.rope_norm_backward(again(g), again(x), pos, (hd // 2,), w)
+    assert torch.equal(dx, again(dx1))
+    # 552 u (sums) and 40 u (terms) of the terms' magnitudes
+    x64 = x.double()
+    n = x64 / (x64.square().mean((-2, -1), keepdim=True) + 1e-6).sqrt()
+    size = (g.double().abs()[..., 0::2] + g.double().abs()[..., 1::2]).repeat_interleave(2, -1)
+    bound = (size * n.abs()).sum((0, 1)).flatten() * (L // 1000)
+    assert torch.all((dw.double() - dw1.double() * (L // 1000)).abs() <= 600 * 2.0 ** -24 * bound)
