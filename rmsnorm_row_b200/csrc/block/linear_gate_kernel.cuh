@@ -314,8 +314,7 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
     bool ok = true;
     for (uint32_t t = first; ok && t < p.tiles; t += step, ++n) {
       const uint32_t acc = n & 1, round = (n >> 1) & 1;
-      if (!(ok = mbar_wait(smem_u32(&sums_full[acc]), round, &failed))) break;
-      __syncwarp();
+      if (!(ok = warp_wait(smem_u32(&sums_full[acc]), round, &failed))) break;
       tc_fence_after();
       const Tile at = tile_at(p, t);
       const uint32_t row0 = row_of(at);
@@ -343,7 +342,7 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(map_to(smem_u32(&sums_empty[acc]), 0));
         }
-        if (p.has_residual && !(ok = mbar_wait(bars + 8 * buf, (chunk / kBoxes) & 1, &failed))) break;
+        if (p.has_residual && !(ok = warp_wait(bars + 8 * buf, (chunk / kBoxes) & 1, &failed))) break;
         __syncwarp();
         // row `lane` of the box: 64 bytes, 16-byte pieces swizzled as TMA's 64-byte mode has them
         const uint32_t row = boxes + buf * kBoxBytes + lane * 64;
@@ -465,7 +464,7 @@ linear_gate_split(const __grid_constant__ LinearParams p, const __grid_constant_
       if (ok) mma_commit<CG>(smem_u32(&sums_full), leader);
     }
   } else {
-    mbar_wait(smem_u32(&sums_full), 0, &failed);  // every product is done, and every copy has been used
+    warp_wait(smem_u32(&sums_full), 0, &failed);  // every product is done, and every copy has been used
     tc_fence_after();
   }
   __syncwarp();

@@ -84,6 +84,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same for a whole warp, whose lanes go on or give up together.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, failed));
+}
+
 // ---- TMA --------------------------------------------------------------------------------------
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
