@@ -467,8 +467,13 @@ linear_gate_split(const __grid_constant__ LinearParams p, const __grid_constant_
     warp_wait(smem_u32(&sums_full), 0, &failed);  // every product is done, and every copy has been used
     tc_fence_after();
   }
+  // A wait that ran out in one CTA leaves copies in flight and sums undone: the whole cluster is told,
+  // and neither exchanges nor stores.
   __syncwarp();
-  cluster_sync();  // now no stage of the cluster is in use
+  if (*(volatile int*)&failed && lane < (int)size) set_remote(map_to(smem_u32(&failed), lane), 1);
+  __syncwarp();
+  cluster_sync();  // now no stage of the cluster is in use, unless `gave_up`
+  const bool gave_up = *(volatile int*)&failed;
 
   constexpr uint32_t kHalf = Shape::kChunks / 2;
   const int quarter = warp & 3;
@@ -480,7 +485,7 @@ linear_gate_split(const __grid_constant__ LinearParams p, const __grid_constant_
     return stages + ((((from < to ? from : from - 1) * each + (j - first_of(to))) * 4 + quarter) * 8 * 32 + lane) * 16;
   };
   const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-  if (warp >= 2) {
+  if (warp >= 2 && !gave_up) {
     for (uint32_t j = first; j < first + kHalf; ++j) {
       const uint32_t to = owner_of(j);
       if (to == mine) continue;
@@ -493,7 +498,7 @@ linear_gate_split(const __grid_constant__ LinearParams p, const __grid_constant_
     }
   }
   cluster_sync();
-  if (warp >= 2) {
+  if (warp >= 2 && !gave_up) {
     const uint32_t row0 = (at.m * CG + side) * kTileM + quarter * 32;
     const bool live = row0 + lane < p.batch_rows;
     const RowOut r = row_out(p, live ? at.batch * p.batch_rows + row0 + lane : 0u);

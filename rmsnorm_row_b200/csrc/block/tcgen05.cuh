@@ -32,6 +32,9 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void store_remote(uint32_t to, float a, float b, float c, float d) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
+__device__ __forceinline__ void set_remote(uint32_t to, int v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
+}
 // A shared-memory address of this CTA as the same place in the cluster's CTA `rank`.
 __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
   uint32_t r;
