@@ -14,8 +14,8 @@
  * immutable handles that several threads and streams may use at once, launches that are
  * asynchronous on the caller's stream and go to the calling thread's current device (the
  * one that owns the stream and the buffers), argument errors found on the host before
- * anything is launched, outputs untouched on an error, no allocation, no synchronisation,
- * no fallback. All buffers are the caller's. Sizes with a zero are valid and launch
+ * anything is launched, outputs untouched on an error, no allocation (but four bytes of host
+ * memory that linear_gate's first launch takes for good), no synchronisation, no fallback. All buffers are the caller's. Sizes with a zero are valid and launch
  * nothing. A non-zero stride need not be larger than the extent it steps over on inputs
  * (rows may overlap); output rows must not overlap each other or an input, except where a
  * call says so.
@@ -211,9 +211,12 @@ fn_status linear_gate_create(linear_gate_t* out, const lg_config* cfg);
 fn_status linear_gate_validate(linear_gate_t h, const lg_args* a);
 /* One kernel launch. */
 fn_status linear_gate_launch(linear_gate_t h, const lg_args* a, fn_stream_t stream);
-/* The matrix kernel bounds its internal waits (ten seconds); a launch in which one ran out, a
- * sign of a broken device, leaves its output incomplete and is counted on its device. Reads the
- * current device's count (synchronises with its default stream). */
+/* The matrix kernel bounds its internal waits (ten seconds of wall clock, in which the device may
+ * also have been busy with another process); a launch in which one ran out leaves its output
+ * incomplete. The next linear_gate_launch of the process, on any device, then launches nothing and
+ * returns FN_ERR_CUDA with cudaErrorLaunchTimeout (702) as the last error, once; and the CTAs in
+ * which it happened are counted on their device, for replayed graphs too. This call reads the
+ * current device's count (and synchronises with its default stream). */
 fn_status linear_gate_timeouts(int* count);
 fn_status linear_gate_destroy(linear_gate_t h);
 

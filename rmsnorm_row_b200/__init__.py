@@ -23,7 +23,7 @@ from ._abi import (FN_ERR_CUDA, FN_ERR_INVALID_ARG, FN_ERR_MISALIGNED, FN_ERR_UN
                    fused_norm_launch, fused_norm_plan, fused_norm_status_string,
                    fused_norm_validate, fused_norm_version, load)
 from .api import build_args, fused_residual_norm_scale_shift, norm_scale_shift
-from .linear import linear_gate_residual
+from .linear import linear_gate_residual, linear_gate_timeouts
 from .norm_quant import fused_residual_norm_scale_shift_quant, norm_scale_shift_quant
 from .rope import rope_norm, rope_norm_backward
 
@@ -34,5 +34,5 @@ __all__ = [
     "fused_norm_launch", "fused_norm_plan", "fused_norm_status_string", "fused_norm_validate",
     "fused_norm_version", "build_args", "fused_residual_norm_scale_shift", "norm_scale_shift",
     "fused_residual_norm_scale_shift_quant", "norm_scale_shift_quant",
-    "rope_norm", "rope_norm_backward", "linear_gate_residual",
+    "rope_norm", "rope_norm_backward", "linear_gate_residual", "linear_gate_timeouts",
 ]

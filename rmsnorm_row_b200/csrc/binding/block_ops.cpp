@@ -41,7 +41,11 @@ Raised ValueError(const char* format, A... a) {
 void check_status(fn_status s, const char* what) {
   if (s == FN_OK) return;
   std::string detail = block_ops_status_string(s);
-  if (s == FN_ERR_CUDA) detail += " (cudaError " + std::to_string(block_ops_last_cuda_error()) + ")";
+  if (s == FN_ERR_CUDA) {
+    const int e = block_ops_last_cuda_error();
+    detail += " (cudaError " + std::to_string(e) + ")";
+    if (e == cudaErrorLaunchTimeout) detail += ": a wait of an earlier linear_gate_residual ran out, its output is incomplete";
+  }
   PyObject* e = PyObject_CallFunction(g_error, "iss", (int)s, what, detail.c_str());
   if (e) {
     PyErr_SetObject(g_error, e);

@@ -81,4 +81,7 @@ inline bool same_rows(const fn_operand& o, const void* p, int64_t sb, int64_t sl
 // Keeps the runtime's status of this thread's last failed launch; FN_OK or FN_ERR_CUDA.
 fn_status launch_status(int cuda_error);
 
+// FN_ERR_CUDA (cudaErrorLaunchTimeout), once, after a kernel has set *gave_up; FN_OK otherwise.
+fn_status wait_status(int* gave_up);
+
 }  // namespace block_ops

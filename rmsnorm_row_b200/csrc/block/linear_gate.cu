@@ -79,6 +79,22 @@ fn_status validate(const linear_gate_s* h, const lg_args* a) {
   return FN_OK;
 }
 
+// Where the matrix kernels say that a wait ran out: four bytes of host memory that every device
+// maps, for the life of the process. nullptr if there is none. The first call may be captured.
+int* gave_up_word() {
+  static int* const word = []() -> int* {
+    void* at = nullptr;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    const cudaError_t e = cudaHostAlloc(&at, sizeof(int), cudaHostAllocPortable | cudaHostAllocMapped);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return nullptr;
+    *static_cast<int*>(at) = 0;
+    return static_cast<int*>(at);
+  }();
+  return word;
+}
+
 LinearOperand operand_of(const fn_operand& o) {
   return LinearOperand{static_cast<const uint16_t*>(o.ptr), o.stride_b, o.stride_f, o.stride_l};
 }
@@ -332,6 +348,10 @@ fn_status linear_gate_launch(linear_gate_t h, const lg_args* a, fn_stream_t stre
   const fn_status s = validate(h, a);
   if (s != FN_OK || a->B == 0 || a->L == 0) return s;
   LinearParams p = make_params(h, a);
+  p.gave_up = gave_up_word();
+  if (!p.gave_up) return launch_status(cudaErrorMemoryAllocation);
+  const fn_status before = wait_status(p.gave_up);
+  if (before != FN_OK) return before;
   if (p.rows <= (uint32_t)kTokens) return launch_tokens(h, p, reinterpret_cast<cudaStream_t>(stream));
   return launch_tiles(h, a, p, reinterpret_cast<cudaStream_t>(stream));
 }

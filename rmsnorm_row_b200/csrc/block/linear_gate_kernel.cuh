@@ -52,6 +52,7 @@ struct LinearParams {
   const float *x_scale, *weight_scale;
   uint16_t* out;
   int64_t out_sb, out_sl;
+  int* gave_up;  // host memory: set when a wait ran out
 };
 
 // ---- the epilogue -----------------------------------------------------------------------------
@@ -205,7 +206,14 @@ __device__ __forceinline__ Tile tile_at(const LinearParams& p, uint32_t t) {
   return Tile{b, m - b * p.tiles_m, n};
 }
 
-__device__ int linear_gate_gave_up = 0;  // launches in which a wait ran out (this file is included once)
+__device__ int linear_gate_gave_up = 0;  // CTAs in which a wait ran out (this file is included once)
+
+// A wait of this CTA ran out (one thread): counted here, and said to the host's next call.
+__device__ __forceinline__ void say_gave_up(const LinearParams& p) {
+  atomicAdd(&linear_gate_gave_up, 1);
+  *(volatile int*)p.gave_up = 1;
+  __threadfence_system();
+}
 
 template <int CG, int BN, bool FP8, bool FP16>
 __global__ void __launch_bounds__(kMatrixThreads, 1)
@@ -376,7 +384,7 @@ linear_gate_tiles(const __grid_constant__ LinearParams p, const __grid_constant_
   tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync();
-  if (threadIdx.x == 0 && failed) atomicAdd(&linear_gate_gave_up, 1);
+  if (threadIdx.x == 0 && failed) say_gave_up(p);
   if (warp == 1) {
     tc_fence_after();
     tmem_free<CG>(tmem, S::kColumns);
@@ -541,7 +549,7 @@ linear_gate_split(const __grid_constant__ LinearParams p, const __grid_constant_
   tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync();
-  if (threadIdx.x == 0 && failed) atomicAdd(&linear_gate_gave_up, 1);
+  if (threadIdx.x == 0 && failed) say_gave_up(p);
   if (warp == 1) {
     tc_fence_after();
     tmem_free<CG>(tmem, BN);

@@ -11,6 +11,11 @@ fn_status launch_status(int cuda_error) {
   g_last_cuda_error = cuda_error;
   return FN_ERR_CUDA;
 }
+
+fn_status wait_status(int* gave_up) {
+  if (!__atomic_load_n(gave_up, __ATOMIC_RELAXED) || !__atomic_exchange_n(gave_up, 0, __ATOMIC_ACQ_REL)) return FN_OK;
+  return launch_status(cudaErrorLaunchTimeout);
+}
 }  // namespace block_ops
 
 extern "C" {

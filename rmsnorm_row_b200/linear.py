@@ -13,13 +13,18 @@ that the norm ops accept: (N,), (1, N), (1, 1, N), (B, N), (B, 1, N), (B, L, N) 
 K and N are multiples of 8 (K of 16 for e4m3). activation is "none", "silu", "gelu" or
 "gelu_tanh". Sums are fp32; out is rounded once. Streams and devices are those of the package's
 other ops.
+
+The matrix kernel bounds its internal waits. A call in which one ran out (ten seconds) leaves its
+output incomplete: the next call raises FusedNormError, and ``linear_gate_timeouts`` counts it.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
 
+from . import _block_abi
 from ._block_abi import binding
 
 
@@ -30,3 +35,12 @@ def linear_gate_residual(x: torch.Tensor, weight: torch.Tensor, bias: Optional[t
                          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """residual + gate * activation(x @ weight.T + bias). `out` may be residual itself."""
     return binding().linear_gate(x, weight, bias, gate, residual, activation, x_scale, weight_scale, out, stream)
+
+
+def linear_gate_timeouts(device: Optional[torch.device] = None) -> int:
+    """How many CTAs of linear_gate_residual on `device` (default: the current one) have given up a wait
+    since the library was loaded. Synchronises with the device's default stream."""
+    n = ctypes.c_int()
+    with torch.cuda.device(device):
+        _block_abi.check(_block_abi.load().linear_gate_timeouts(ctypes.byref(n)), "linear_gate_timeouts")
+    return n.value
