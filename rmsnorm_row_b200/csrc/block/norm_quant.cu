@@ -419,6 +419,11 @@ Shape shape_of(int D) {
   return Shape{(V + T - 1) / T, T};
 }
 
+// Shared memory that the widest rows keep. A kernel's limit is set to that, whatever the handle: handles
+// of several widths share a kernel, and another host thread may be between its limit and its launch.
+constexpr int kMaxKept = 5 * 16 * kMaxVectors * 416;
+static_assert(16384 / 8 <= kMaxVectors * 416 && kMaxKept + sizeof(GroupShared) * kMaxWarps <= 227 * 1024, "rows of 16384 channels fit");
+
 using Kernel = void (*)(QuantParams);
 
 template <bool RMS, bool SHARED, bool MOD, bool ADD>
@@ -582,7 +587,7 @@ fn_status norm_quant_launch(norm_quant_t h, const nq_args* a, fn_stream_t stream
     p.div_segment = make_div_u32(p.segment);
     cfg.blockDim = dim3(T, groups);
     cfg.dynamicSmemBytes = h->kept;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)h->kept);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKept);
     if (e != cudaSuccess) return launch_status(e);
   } else {
     kernel = p.scale ? h->each_mod : h->each;

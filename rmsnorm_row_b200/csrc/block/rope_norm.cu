@@ -233,10 +233,11 @@ RopeRows rows_of(const rn_rows& r) {
   return RopeRows{static_cast<const uint16_t*>(r.ptr), r.stride_b, r.stride_l, r.stride_h};
 }
 
-// Above 48 KB a kernel's shared memory is asked for, once per device context.
+// Above 48 KB a kernel's shared memory is asked for: all there is, whatever the handle needs, since
+// another host thread may be launching the same kernel for a handle that needs more.
 cudaError_t allow_shared(const RopeShape& s) {
   if (s.smem <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(s.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
+  return cudaFuncSetAttribute(s.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxShared);
 }
 
 fn_status sms_of(int* sms) {

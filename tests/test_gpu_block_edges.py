@@ -1,9 +1,13 @@
 """GPU tests of the operators of include/block_ops.h at the edges of their calls: row slots
 without a row, long sums, rare values, calls from several host threads, autograd."""
+import ctypes
+import threading
+
 import pytest
 import torch
 
 import rmsnorm_row_b200 as fn
+from rmsnorm_row_b200 import _block_abi
 
 pytestmark = pytest.mark.gpu
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -118,3 +122,58 @@ def test_runs_of_dweight_add_up():
     size = (g.double().abs()[..., 0::2] + g.double().abs()[..., 1::2]).repeat_interleave(2, -1)
     bound = (size * n.abs()).sum((0, 1)).flatten() * (L // 1000)
     assert torch.all((dw.double() - dw1.double() * (L // 1000)).abs() <= 600 * 2.0 ** -24 * bound)
+
+
+# ---- several host threads --------------------------------------------------------------------------
+
+def launches_of_rows(D):
+    """(a launch of norm_quant for rows of D channels through the C ABI, the tensors it needs)"""
+    lib, rows = _block_abi.load(), 1300
+    x, q = rand(1, rows, D), torch.empty(1, rows, D, device="cuda", dtype=torch.float8_e4m3fn)
+    s = torch.empty(1, rows, device="cuda")
+    h = ctypes.c_void_p()
+    assert lib.norm_quant_create(ctypes.byref(h), ctypes.byref(_block_abi.nq_config(D=D, is_rms=1, eps=1e-6))) == fn.FN_OK
+    a = _block_abi.nq_args()
+    a.B, a.L, a.x = 1, rows, fn.fn_operand(x.data_ptr(), 0, 0, D)
+    a.q, a.q_stride_b, a.q_stride_l, a.row_scale = q.data_ptr(), rows * D, D, s.data_ptr()
+    return (lambda stream: lib.norm_quant_launch(h, ctypes.byref(a), stream)), (x, q, s, a)
+
+
+def launches_of_rotation(H, backward):
+    lib, rows, D = _block_abi.load(), 700, H * 128
+    x, y, w = rand(1, rows, H, 128), torch.empty(1, rows, H, 128, device="cuda", dtype=BF), rand(D)
+    pos = torch.zeros(rows, 1, device="cuda", dtype=torch.int32)
+    h = ctypes.c_void_p()
+    c = _block_abi.rn_config(dtype=0, heads=H, head_dim=128, axes=1, section=(64, 0, 0, 0), norm=2, has_weight=1, theta=1e4, eps=1e-6)
+    assert lib.rope_norm_create(ctypes.byref(h), ctypes.byref(c)) == fn.FN_OK
+    r = lambda t: _block_abi.rn_rows(t.data_ptr(), rows * D, D, 128)
+    if not backward:
+        a = _block_abi.rn_args(1, rows, r(x), pos.data_ptr(), 0, 1, w.data_ptr(), r(y))
+        return (lambda stream: lib.rope_norm_launch(h, ctypes.byref(a), stream)), (x, y, w, pos, a)
+    n = ctypes.c_uint64()
+    assert lib.rope_norm_backward_workspace(h, 1, rows, ctypes.byref(n)) == fn.FN_OK
+    work, dw = torch.empty(n.value, device="cuda", dtype=torch.uint8), torch.empty(D, device="cuda")
+    a = _block_abi.rn_backward_args(1, rows, r(x), r(x), pos.data_ptr(), 0, 1, w.data_ptr(), r(y), dw.data_ptr(), work.data_ptr(), n.value)
+    return (lambda stream: lib.rope_norm_backward_launch(h, ctypes.byref(a), stream)), (x, y, w, pos, work, dw, a)
+
+
+@pytest.mark.parametrize("make,sizes", [(launches_of_rows, [(5120,), (10240,)]), (launches_of_rotation, [(128, False), (100, False)]),
+                                        (launches_of_rotation, [(128, True), (100, True)])])
+def test_two_host_threads_launch_different_sizes(make, sizes):
+    """Two handles whose sizes share a kernel, launched by two host threads at once: every call is valid."""
+    calls = [make(*size) for size in sizes]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    status = [set(), set()]
+
+    def run(i):
+        for _ in range(20000):
+            status[i].add(calls[i][0](streams[i].cuda_stream))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert status == [{fn.FN_OK}, {fn.FN_OK}]
