@@ -60,6 +60,34 @@ struct LinearParams {
 // z sigmoid(s z') forms: the quotient of a huge |z| and e^|z| is 0, of an infinity NaN.
 __device__ __forceinline__ float logistic_times(float z, float e) { return __fdividef(z, 1.0f + __expf(-e)); }
 
+// GELU z Phi(z) of two values. Phi(-|z|) = erfc(|z| / sqrt 2) / 2 = e^(-z^2 / 2) s Q(s) with
+// s = 1 / (1 + 0.212 |z|): Q is the polynomial of degree 8 with the least largest relative error, 2e-8,
+// over |z| <= 13.5 (fitted by reweighted least squares). 1 + erf(z / sqrt 2) loses the value where
+// z < 0, and erfcf, as good, takes longer: 50000 x 2048 x 4096 553 us, with erff 570, with erfcf 698.
+// e^(-z^2 / 2) below 2^-126 (z < -13.2) is 0.
+__device__ __forceinline__ uint64_t gelu(uint64_t z) {
+  using namespace fused_norm_impl;
+  auto both = [](float v) { return pk2(v, v); };
+  float z0, z1, a0, a1, e0, e1;
+  upk2(z, z0, z1);
+  upk2(fma2(pk2(fabsf(z0), fabsf(z1)), both(0.212132037f), both(1.0f)), a0, a1);
+  const uint64_t s = pk2(__fdividef(1.0f, a0), __fdividef(1.0f, a1));
+  uint64_t h = both(-0.064728424f);
+  h = fma2(h, s, both(0.242608264f));
+  h = fma2(h, s, both(-0.255749017f));
+  h = fma2(h, s, both(0.273369312f));
+  h = fma2(h, s, both(-0.0469483174f));
+  h = fma2(h, s, both(0.107282139f));
+  h = fma2(h, s, both(0.0742224231f));
+  h = fma2(h, s, both(0.0853490382f));
+  h = fma2(h, s, both(0.0845945925f));
+  upk2(mul2(mul2(z, z), both(-0.72134752f)), e0, e1);  // z^2 log2(e) / 2
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e0));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e1));
+  upk2(mul2(mul2(h, s), pk2(e0, e1)), a0, a1);
+  return mul2(z, pk2(z0 > 0.0f ? 1.0f - a0 : a0, z1 > 0.0f ? 1.0f - a1 : a1));
+}
+
 template <int N>
 __device__ __forceinline__ void activate(int act, float (&v)[N]) {
   if (act == BO_ACT_NONE) return;
@@ -68,7 +96,10 @@ __device__ __forceinline__ void activate(int act, float (&v)[N]) {
     for (int i = 0; i < N; ++i) v[i] = logistic_times(v[i], v[i]);
   } else if (act == BO_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678118654752f));
+    for (int i = 0; i < N; i += 2) {
+      float unused;
+      fused_norm_impl::upk2(gelu(fused_norm_impl::pk2(v[i], v[N > 1 ? i + 1 : i])), v[i], N > 1 ? v[i + 1] : unused);
+    }
   } else {  // 1/2 (1 + tanh t) = 1 / (1 + e^-2t)
 #pragma unroll
     for (int i = 0; i < N; ++i) {

@@ -177,3 +177,27 @@ def test_two_host_threads_launch_different_sizes(make, sizes):
         t.join()
     torch.cuda.synchronize()
     assert status == [{fn.FN_OK}, {fn.FN_OK}]
+
+
+# ---- linear_gate -------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("rows", [2, 64, 5000])
+@pytest.mark.parametrize("activation", ["gelu", "silu"])
+def test_activations_far_below_zero(activation, rows, dtype):
+    """x W^T is the bias alone, so z is exact. z Phi(z) = z erfc(-z / sqrt 2) / 2: the argument is off by
+    one rounding and the product by another, 2 u of it, which erfc's exponent turns into at most
+    2 (z^2 / 2 + 1) 2 u, and erfcf is good to 6 ulp: (2 z^2 + 16) u. SiLU: e^-z is off by (2 + 2 |z|) ulp
+    (__expf), the quotient by 2 ulp: (2 |z| + 8) 2 u. Then half a step of the type; below its normal
+    numbers half of its smallest."""
+    z = torch.arange(-12, 4, 0.125, device="cuda").to(dtype)
+    x, w = torch.zeros(1, rows, 64, device="cuda", dtype=dtype), torch.zeros(z.numel(), 64, device="cuda", dtype=dtype)
+    out = fn.linear_gate_residual(x, w, z, activation=activation)
+    v = z.double()
+    if activation == "gelu":
+        want, u = 0.5 * v * torch.special.erfc(-v / 2 ** 0.5), 2 * v * v + 16
+    else:
+        want, u = v / (1 + (-v).exp()), 4 * v.abs() + 16
+    info = torch.finfo(dtype)
+    bound = want.abs() * (info.eps / 2 + u * 2.0 ** -24) + info.smallest_normal * info.eps / 2
+    assert torch.all((out.double() - want).abs() <= bound)
