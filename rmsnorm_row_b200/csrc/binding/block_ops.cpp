@@ -166,9 +166,11 @@ bool truth(PyObject* o) {
 Tensor empty(c10::IntArrayRef shape, at::ScalarType dtype, const at::Device& device) {
   return at::detail::empty_cuda(shape, dtype, device, std::nullopt);
 }
+// The result as Python has it; autograd is told that a tensor of the caller's has changed.
 PyObject* wrap(PyObject* given, const Tensor& t) {
-  if (given != Py_None) return Py_NewRef(given);
-  return THPVariable_Wrap(t);
+  if (given == Py_None) return THPVariable_Wrap(t);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  return Py_NewRef(given);
 }
 
 // The device and stream of a call: x's device, and the caller's torch.cuda.Stream or the current

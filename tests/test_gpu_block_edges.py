@@ -201,3 +201,45 @@ def test_activations_far_below_zero(activation, rows, dtype):
     info = torch.finfo(dtype)
     bound = want.abs() * (info.eps / 2 + u * 2.0 ** -24) + info.smallest_normal * info.eps / 2
     assert torch.all((out.double() - want).abs() <= bound)
+
+
+# ---- autograd ------------------------------------------------------------------------------------------
+
+def written():
+    """Every call with tensors of the caller's for its results: (name, call, those tensors)."""
+    x, w, res = rand(1, 40, 64), rand(64, 64, seed=1), rand(1, 40, 64, seed=2)
+    q, s, r = torch.empty(1, 40, 64, device="cuda", dtype=torch.float8_e4m3fn), torch.empty(1, 40, device="cuda"), torch.empty_like(x)
+    h, pos = x.view(1, 40, 2, 32), torch.zeros(40, 1, device="cuda", dtype=torch.int32)
+    y, dx = torch.empty_like(h), torch.empty_like(h)
+    return [
+        ("rows", lambda: fn.norm_scale_shift_quant(x, None, None, None, None, out=q, row_scale_out=s), [q, s]),
+        ("residual rows", lambda: fn.fused_residual_norm_scale_shift_quant(res, x, None, None, None, None, None, residual_out=r), [r]),
+        ("residual in place", lambda: fn.fused_residual_norm_scale_shift_quant(res, x, None, None, None, None, None, residual_out=res), [res]),
+        ("rotation", lambda: fn.rope_norm(h, pos, (16,), out=y), [y]),
+        ("gradient", lambda: fn.rope_norm_backward(h, h, pos, (16,), out=dx), [dx]),
+        ("product", lambda: fn.linear_gate_residual(x, w, residual=res, out=res), [res]),
+    ]
+
+
+def test_written_tensors_count_as_changed():
+    """A tensor that autograd has saved and that a call then writes fails the backward pass, as with any in-place op."""
+    for name, call, outs in written():
+        before = [t._version for t in outs]
+        call()
+        assert [t._version for t in outs] == [v + 1 for v in before], name
+    a = torch.ones(1, 40, 64, device="cuda", dtype=BF, requires_grad=True)
+    res = rand(1, 40, 64)
+    loss = (a * res).sum()
+    fn.linear_gate_residual(rand(1, 40, 64), rand(64, 64), residual=res, out=res)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        for name, call, outs in written():
+            call()
+
+
+def test_results_require_no_gradient():
+    x, w = rand(1, 40, 64).requires_grad_(), rand(64, 64).requires_grad_()
+    h, pos = x.view(1, 40, 2, 32), torch.zeros(40, 1, device="cuda", dtype=torch.int32)
+    for out in (fn.linear_gate_residual(x, w), fn.norm_scale_shift_quant(x, None, None, None, None)[1], fn.rope_norm(h, pos, (16,))):
+        assert not out.requires_grad and out.grad_fn is None
