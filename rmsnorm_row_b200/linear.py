@@ -12,7 +12,8 @@ x * x_scale and weight * weight_scale. bias is (N,), residual (B, L, N); gate ha
 that the norm ops accept: (N,), (1, N), (1, 1, N), (B, N), (B, 1, N), (B, L, N) or (B or 1, F, 1, N).
 K and N are multiples of 8 (K of 16 for e4m3). activation is "none", "silu", "gelu" or
 "gelu_tanh". Sums are fp32; out is rounded once. Streams and devices are those of the package's
-other ops.
+other ops. The function is not recorded by autograd: its result requires no gradient, whatever its
+inputs do.
 
 The matrix kernel bounds its internal waits. A call in which one ran out (ten seconds) leaves its
 output incomplete: the next call raises FusedNormError, and ``linear_gate_timeouts`` counts it.

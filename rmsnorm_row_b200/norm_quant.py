@@ -13,7 +13,8 @@ y, which is what ``linear_gate_residual`` takes as x and x_scale:
     q = e4m3(y / row_scale)
 
 Operand shapes, dtypes, streams and devices are those of the 16-bit ops; D may be any multiple
-of 16 up to 16384, and scale and shift may both be None (no modulation).
+of 16 up to 16384, and scale and shift may both be None (no modulation). The functions are not
+recorded by autograd: their results require no gradient, whatever their inputs do.
 """
 from __future__ import annotations
 

@@ -14,8 +14,8 @@ or "none"; weight is optional, of x's dtype or fp32. pairing is "interleaved" (c
 2i + 1) or "half" (i and i + sum(sections)). Each section has frequencies theta^(-i / pairs of
 the section), or, with shared_frequencies, pair i of all has theta^(-i / sum(sections)).
 
-The functions are not recorded by autograd: a training step calls rope_norm_backward with the
-forward's inputs. Streams and devices are those of the package's other ops.
+The functions are not recorded by autograd (their results require no gradient): a training step
+calls rope_norm_backward with the forward's inputs. Streams and devices are those of the package's other ops.
 """
 from __future__ import annotations
 
