@@ -11,6 +11,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <string>
@@ -196,16 +197,26 @@ class Place {
   fn_stream_t handle_;
 };
 
-// One handle per configuration and process. Configurations are zeroed before they are filled,
-// so their bytes compare; the interpreter's lock guards the list.
+// Handles of the configurations used last, the latest first. Configurations are zeroed before they
+// are filled, so their bytes compare; the interpreter's lock guards the list. A launch keeps nothing
+// of its handle, so one whose configuration has not come for kHandles others is given up (theta and
+// eps are part of a configuration: a program may change them with each length).
+constexpr size_t kHandles = 64;
 template <typename Config, typename Handle>
-Handle handle_for(const Config& c, fn_status (*create)(Handle*, const Config*), const char* what) {
+Handle handle_for(const Config& c, fn_status (*create)(Handle*, const Config*), fn_status (*destroy)(Handle), const char* what) {
   static std::vector<std::pair<Config, Handle>> known;
-  for (const auto& k : known)
-    if (std::memcmp(&k.first, &c, sizeof(c)) == 0) return k.second;
+  for (size_t i = 0; i < known.size(); ++i)
+    if (std::memcmp(&known[i].first, &c, sizeof(c)) == 0) {
+      std::rotate(known.begin(), known.begin() + i, known.begin() + i + 1);
+      return known.front().second;
+    }
   Handle h;
   check_status(create(&h, &c), what);
-  known.emplace_back(c, h);
+  if (known.size() == kHandles) {
+    destroy(known.back().second);
+    known.pop_back();
+  }
+  known.emplace(known.begin(), c, h);
   return h;
 }
 template <typename T>
@@ -288,7 +299,7 @@ ENTRY(norm_quant, 13) {
   if (!s.is_contiguous()) throw ValueError("row_scale_out must be contiguous");
   g.q = q.data_ptr(), g.q_stride_b = q.stride(0), g.q_stride_l = q.stride(1);
   g.row_scale = static_cast<float*>(s.data_ptr());
-  const norm_quant_t h = handle_for(c, norm_quant_create, "norm_quant_create");
+  const norm_quant_t h = handle_for(c, norm_quant_create, norm_quant_destroy, "norm_quant_create");
   check_status(norm_quant_launch(h, &g, place.stream()), "norm_quant_launch");
   PyObject* out = PyTuple_New(residual ? 3 : 2);
   if (!out) throw Raised();
@@ -371,7 +382,7 @@ RopeCall rope_call(const Tensor& x, PyObject* const* a) {
     c.has_weight = 1;
     c.weight_fp32 = weight->scalar_type() == at::kFloat;
   }
-  r.h = handle_for(c, rope_norm_create, "rope_norm_create");
+  r.h = handle_for(c, rope_norm_create, rope_norm_destroy, "rope_norm_create");
   return r;
 }
 
@@ -472,7 +483,7 @@ ENTRY(linear_gate, 10) {
   check_shape(out, "out", {B, L, N}, dtype, device);
   check_tensor(out, "out", device, dtype);
   g.out = out.data_ptr(), g.out_stride_b = out.stride(0), g.out_stride_l = out.stride(1);
-  const linear_gate_t h = handle_for(c, linear_gate_create, "linear_gate_create");
+  const linear_gate_t h = handle_for(c, linear_gate_create, linear_gate_destroy, "linear_gate_create");
   check_status(linear_gate_launch(h, &g, place.stream()), "linear_gate_launch");
   return wrap(a[8], out);
 }

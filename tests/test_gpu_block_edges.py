@@ -243,3 +243,23 @@ def test_results_require_no_gradient():
     h, pos = x.view(1, 40, 2, 32), torch.zeros(40, 1, device="cuda", dtype=torch.int32)
     for out in (fn.linear_gate_residual(x, w), fn.norm_scale_shift_quant(x, None, None, None, None)[1], fn.rope_norm(h, pos, (16,))):
         assert not out.requires_grad and out.grad_fn is None
+
+
+# ---- handles -------------------------------------------------------------------------------------------
+
+def test_configurations_that_change_with_each_call_do_not_pile_up():
+    """20000 thetas and epsilons: the process keeps a bounded number of handles (2.4 KB each), and calls
+    with a configuration given up long ago, or just now, are right."""
+    x, pos = rand(1, 3, 2, 32), torch.arange(3, device="cuda", dtype=torch.int32)[:, None]
+    call = lambda i: fn.rope_norm(x, pos, (16,), norm="head", theta=1000.0 + i, eps=1e-6 * (1 + i))
+    first, last = call(0), call(20000)
+    resident = lambda: int(open("/proc/self/statm").read().split()[1]) * 4096
+    for i in range(1, 200):
+        call(i)
+    torch.cuda.synchronize()
+    before = resident()
+    for i in range(200, 20001):
+        out = call(i)
+    torch.cuda.synchronize()
+    assert resident() - before < 16 << 20
+    assert torch.equal(out, last) and torch.equal(call(0), first) and not torch.equal(first, last)
