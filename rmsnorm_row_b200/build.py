@@ -9,12 +9,14 @@ GPU and no CUDA shared libraries beyond the driver at launch time.
 Precise division and square root are kept (no fast-math).
 
 csrc/binding/ is the Python side of the operators of include/block_ops.h, a CPython extension
-(_binding.so) against the installed PyTorch that links to the library.
+(_binding.so) against the installed PyTorch that links to the library. Without PyTorch only the
+library is built, which is all that C programs need (the Python package needs PyTorch anyway).
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -52,6 +54,10 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _torch_is_installed() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
 def _build_binding() -> None:
     import sysconfig
 
@@ -73,26 +79,29 @@ def _build_binding() -> None:
     os.replace(tmp, BINDING)
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _stale(target: str) -> bool:
+    if not os.path.exists(target):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = os.path.getmtime(target)
     srcs = glob.glob(os.path.join(CSRC, "**", "*"), recursive=True) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
     return any(os.path.getmtime(s) > t for s in srcs)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int = 4) -> str:
-    if not force and not _stale():
-        return LIB
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = sorted(glob.glob(os.path.join(CSRC, "**", "*.cu"), recursive=True))
-    with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-    tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp, *objs]
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
-    _build_binding()
+    if force or _stale(LIB):
+        os.makedirs(BUILD_DIR, exist_ok=True)
+        srcs = sorted(glob.glob(os.path.join(CSRC, "**", "*.cu"), recursive=True))
+        with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
+            objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        tmp = LIB + ".tmp"
+        cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp, *objs]
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, LIB)
+        force = True
+    if not _torch_is_installed():
+        print("PyTorch is not installed: _binding.so is left out", file=sys.stderr)
+    elif force or _stale(BINDING):
+        _build_binding()
     return LIB
 
 
