@@ -36,7 +36,8 @@ const char* block_ops_status_string(fn_status s);
  * this host thread; 0 if none. */
 int block_ops_last_cuda_error(void);
 
-/* Element types of the calls below. */
+/* Element types of the calls below. BO_FP32 is that of scales and fp32 weights, which have arguments
+ * of their own: no configuration takes it as its dtype (FN_ERR_UNSUPPORTED). */
 typedef enum { BO_BF16 = 0, BO_FP16 = 1, BO_E4M3 = 2, BO_FP32 = 3 } bo_dtype;
 
 /* ---- norm_quant -----------------------------------------------------------------------

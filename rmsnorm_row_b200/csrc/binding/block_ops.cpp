@@ -71,7 +71,7 @@ std::string shape_of(c10::IntArrayRef s) {
   for (size_t i = 0; i < s.size(); ++i) t += (i ? ", " : "") + std::to_string(s[i]);
   return t + (s.size() == 1 ? ",)" : ")");
 }
-int code_of(at::ScalarType t) { return t == at::kBFloat16 ? BO_BF16 : t == at::kHalf ? BO_FP16 : t == at::kFloat ? BO_FP32 : BO_E4M3; }
+int code_of(at::ScalarType t) { return t == at::kBFloat16 ? BO_BF16 : t == at::kHalf ? BO_FP16 : BO_E4M3; }
 
 const Tensor* tensor(PyObject* o, const char* name, bool optional = false) {
   if (optional && o == Py_None) return nullptr;

@@ -122,12 +122,11 @@ LinearParams make_params(const linear_gate_s* h, const lg_args* a) {
 
 template <int PARTS, bool FP8, bool FP16>
 void* token_kernel(int M) {
-  switch (M) {
-    case 1: return (void*)linear_gate_tokens<1, PARTS, FP8, FP16>;
-    case 2: return (void*)linear_gate_tokens<2, PARTS, FP8, FP16>;
-    case 3: return (void*)linear_gate_tokens<3, PARTS, FP8, FP16>;
-    default: return (void*)linear_gate_tokens<4, PARTS, FP8, FP16>;
+  if constexpr (PARTS == 4) {  // one part is for three and four tokens only
+    if (M == 1) return (void*)linear_gate_tokens<1, PARTS, FP8, FP16>;
+    if (M == 2) return (void*)linear_gate_tokens<2, PARTS, FP8, FP16>;
   }
+  return M == 3 ? (void*)linear_gate_tokens<3, PARTS, FP8, FP16> : (void*)linear_gate_tokens<4, PARTS, FP8, FP16>;
 }
 template <int PARTS>
 void* token_kernel(int dtype, int M) {
