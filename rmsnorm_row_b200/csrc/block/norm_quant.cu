@@ -12,8 +12,9 @@
 // only write, as fp32 (the scale needs the whole row's maximum before anything is quantised).
 //
 // Layout: thread t of the row's T threads owns the 16-byte vectors t, t + T, ... (every warp
-// access is 512 contiguous bytes), at most five. A row meets at two barriers, for its statistics
-// and its maximum; rows of one warp reduce through shuffles alone.
+// access is 512 contiguous bytes), at most five, in 128 registers (LayerNorm with modulation per
+// token, which keeps row, scale and shift, spills 100 bytes). A row meets at two barriers, for its
+// statistics and its maximum; rows of one warp reduce through shuffles alone.
 //
 // Where no operand changes from token to token, CTAs are persistent (one per SM, its threads as
 // groups of T with a row each) and keep gate, weight (1 + scale) and bias (1 + scale) + shift of

@@ -29,7 +29,7 @@ namespace block_ops {
 
 constexpr int kMaxPairs = 256;      // of a head
 constexpr int kRopeThreads = 512;   // of a CTA, at most
-constexpr int kForwardThreads = 384;  // of a forward CTA: 168 registers hold a lane's ten heads
+constexpr int kForwardThreads = 384;  // of a forward CTA: a lane's ten heads in 168 registers, but for 52 bytes (half pairs 72)
 constexpr int kSharedRows = 128;    // threads of a CTA whose rows take 32 lanes or fewer
 constexpr int kMaxPartials = 1024;  // CTAs that sum dweight
 constexpr int kMaxTurns = 512;      // rows (of each slot) that a CTA sums dweight over in a launch
@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(kForwardThreads, 1) rope_norm_rows(const __gri
 // Each thread copies its own vectors of the next row to shared memory while it works on the
 // present one, so no registers wait for loads and nobody else has to be waited for. 128 registers and two
 // stages let three CTAs of a row of 5120 channels run side by side (two with 168 registers or a
-// third stage): 1.08 against 1.24 ms over 176400 tokens.
+// third stage): 1.08 against 1.24 ms over 176400 tokens. Two heads to a thread spill 4 bytes;
+// four, taken where two leave more lanes idle, some 700 with dweight of all heads.
 
 // A thread's own two vectors of a head, in shared memory: x's, then grad's. One stage holds all
 // heads of a thread; vectors of neighbouring threads are neighbours.
