@@ -263,3 +263,39 @@ def test_configurations_that_change_with_each_call_do_not_pile_up():
     torch.cuda.synchronize()
     assert resident() - before < 16 << 20
     assert torch.equal(out, last) and torch.equal(call(0), first) and not torch.equal(first, last)
+
+
+# ---- what runs -----------------------------------------------------------------------------------------
+
+def test_every_call_runs_its_own_kernel_and_nothing_else():
+    """A CUDA activity trace of each call: one kernel of the library, two for a gradient with a weight."""
+    from torch.profiler import ProfilerActivity, profile
+
+    x, w, many = rand(1, 300, 512), rand(256, 512), rand(1, 4000, 512)
+    h, pos, wq = rand(1, 300, 4, 64), torch.zeros(300, 1, device="cuda", dtype=torch.int32), rand(256)
+    long, wide = rand(1, 64, 5120), rand(512, 5120)
+    q, s = fn.norm_scale_shift_quant(rand(1, 256, 512), None, None, None, None)
+    calls = [
+        (lambda: fn.norm_scale_shift_quant(x, None, None, None, None), ["norm_quant_rows"]),
+        (lambda: fn.norm_scale_shift_quant(many, None, None, None, None, "rms"), ["norm_quant_rows"]),
+        (lambda: fn.fused_residual_norm_scale_shift_quant(x, x, None, None, None, None, None), ["norm_quant_rows"]),
+        (lambda: fn.rope_norm(h, pos, (32,), wq), ["rope_norm_rows"]),
+        (lambda: fn.rope_norm_backward(h, h, pos, (32,), wq), ["rope_norm_gradient", "sum_partials"]),
+        (lambda: fn.rope_norm_backward(h, h, pos, (32,), norm="none"), ["rope_norm_rows"]),
+        (lambda: fn.linear_gate_residual(many, w), ["linear_gate_tiles"]),
+        (lambda: fn.linear_gate_residual(long, wide), ["linear_gate_split"]),
+        (lambda: fn.linear_gate_residual(x[:, :2], w), ["linear_gate_tokens"]),
+        (lambda: fn.linear_gate_residual(q, q[0], x_scale=s, weight_scale=s[0]), ["linear_gate"]),
+    ]
+    for call, _ in calls:
+        call()
+    torch.cuda.synchronize()
+    with profile(activities=[ProfilerActivity.CUDA]) as prof:
+        for call, _ in calls:
+            call()
+        torch.cuda.synchronize()
+    ran = [e.name for e in sorted(prof.events(), key=lambda e: e.time_range.start) if e.device_type == torch.autograd.DeviceType.CUDA]
+    if not ran:
+        pytest.skip("no CUDA activity recorded (tracing unavailable)")
+    want = [name for _, names in calls for name in names]
+    assert len(ran) == len(want) and all(w in r for w, r in zip(want, ran)), ran
