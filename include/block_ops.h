@@ -55,7 +55,7 @@ typedef enum { BO_BF16 = 0, BO_FP16 = 1, BO_E4M3 = 2, BO_FP32 = 3 } bo_dtype;
  * taken again in fp64). q is rounded once to nearest even. A row with a = 0 has row_scale 1;
  * a below 2^-100 is taken as 2^-100. A NaN or infinity in y leaves a NaN or infinite
  * row_scale: q is then NaN where y was not finite, and NaN everywhere in a NaN row.
- * 1 / sqrt(variance + eps) has to be below 2^127 (it is for any eps >= 2^-250), and
+ * 1 / sqrt(variance + eps) has to be below 2^127 (it is for any eps >= 2^-250), and r - mean,
  * weight (1 + scale) and bias (1 + scale) + shift, which are formed first, within fp32.
  */
 typedef struct norm_quant_s* norm_quant_t;
@@ -75,7 +75,7 @@ typedef struct {
   int64_t B, L;
   int64_t tokens_per_frame;  /* as in fn_args */
   fn_operand x, residual, gate, scale, shift; /* bf16; ptr NULL where the config has none */
-  const void* weight;        /* (D) */
+  const void* weight;        /* (D), 16-byte aligned, as bias */
   const void* bias;          /* (D) */
   void* q;                   /* (B, L, D) e4m3, 16-byte aligned rows: strides in elements, multiples of 16 */
   int64_t q_stride_b, q_stride_l;
@@ -106,7 +106,8 @@ fn_status norm_quant_destroy(norm_quant_t h);
  * follow axis 0, the next section[1] axis 1, and so on. The i-th of a section's m pairs has
  * freq = theta^(-i / m); with shared_frequencies pair i of all P has theta^(-i / P).
  * Angles are reduced in fp64 (an error of at most |position| 2^-52 turns), all else is fp32,
- * each output is rounded once. A mean square that fp32 does not hold is taken again in fp64.
+ * each output is rounded once. A mean square that fp32 does not hold is taken again in fp64;
+ * rho has to be below 2^127 (it is for any eps >= 2^-250).
  *
  * The gradient, of the same handle: with dn the grad turned back,
  *   dx = rho (w dn - x rho^2 mean(w dn x)),  dweight = sum over tokens (and heads, for
@@ -130,11 +131,11 @@ typedef struct {
   int half_pairs, shared_frequencies;
   int index64;     /* positions are int64_t (otherwise int32_t) */
   double theta;    /* finite, > 0 */
-  double eps;      /* finite, >= 0 */
+  double eps;      /* 0 .. 2^100 */
 } rn_config;
 
 /* Element (b, l, h, c) lies at ptr[b * stride_b + l * stride_l + h * stride_h + c]; strides are
- * multiples of 8 elements, pointers 16-byte aligned. */
+ * multiples of 8 elements, pointers 16-byte aligned, and so is the weight. */
 typedef struct {
   const void* ptr;
   int64_t stride_b, stride_l, stride_h;
@@ -180,7 +181,15 @@ fn_status rope_norm_destroy(rope_norm_t h);
  * x and W are both bf16, both fp16 or both e4m3 (then x W^T is x_scale[row] * weight_scale[n]
  * times the product of the codes, and bias, gate, residual and out are bf16; otherwise they
  * have x's type). The sum over K and everything after it is fp32; out is rounded once. The
- * order of the sum depends on the sizes, not on the run.
+ * order of the sum depends on the sizes, the strides and the device, not on the run: a strided view
+ * and its contiguous copy may differ in the last bit.
+ *
+ * Up to four tokens x may repeat rows (a stride of 0); from five on a stride of 0 along an extent
+ * above 1 is FN_ERR_UNSUPPORTED (a tensor map does not hold it). residual has a row per token at any
+ * size. x_scale * weight_scale, which is formed first, has to be within fp32's normal numbers.
+ * Tokens at one distance throughout, in x, out and residual, are worked on in tiles of 128 or 256;
+ * where batches lie apart (a part of longer rows) a tile stays inside its batch, so many batches of
+ * a few tokens cost up to 128 / L times what the same tokens cost together. Copy them together first.
  * act is SiLU z / (1 + e^-z), GELU z Phi(z), its tanh form, or nothing.
  */
 typedef struct linear_gate_s* linear_gate_t;
@@ -200,7 +209,7 @@ typedef struct {
   fn_operand x;               /* stride_f 0; strides multiples of 16 bytes */
   const void* weight;         /* row n at weight + n * weight_stride elements, 16-byte aligned rows */
   int64_t weight_stride;
-  const void* bias;           /* (N) */
+  const void* bias;           /* (N), 16-byte aligned */
   fn_operand gate, residual;  /* residual: one row per token, stride_f 0 */
   const float* x_scale;       /* (B, L) contiguous; e4m3 */
   const float* weight_scale;  /* (N), 16-byte aligned; e4m3 */

@@ -10,7 +10,10 @@ out is (B, L, N) in x's type, or bf16 for e4m3. e4m3 needs x_scale (B, L), as
 ``norm_scale_shift_quant`` returns it, and weight_scale (N,), both fp32: the product is that of
 x * x_scale and weight * weight_scale. bias is (N,), residual (B, L, N); gate has the shapes
 that the norm ops accept: (N,), (1, N), (1, 1, N), (B, N), (B, 1, N), (B, L, N) or (B or 1, F, 1, N).
-K and N are multiples of 8 (K of 16 for e4m3). activation is "none", "silu", "gelu" or
+K and N are multiples of 8 (K of 16 for e4m3). Rows of x and
+(N,) vectors start at 16 bytes; beyond four tokens x has a row of its own for each (no expanded x).
+Many short batches that lie apart (x[:, :2] of a longer tensor) are slow, up to 128 / L times the
+same tokens in one piece: call .contiguous() on them. activation is "none", "silu", "gelu" or
 "gelu_tanh". Sums are fp32; out is rounded once. Streams and devices are those of the package's
 other ops. The function is not recorded by autograd: its result requires no gradient, whatever its
 inputs do.

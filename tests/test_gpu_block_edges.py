@@ -299,3 +299,29 @@ def test_every_call_runs_its_own_kernel_and_nothing_else():
         pytest.skip("no CUDA activity recorded (tracing unavailable)")
     want = [name for _, names in calls for name in names]
     assert len(ran) == len(want) and all(w in r for w, r in zip(want, ran)), ran
+
+
+# ---- layouts that the documents name -------------------------------------------------------------------
+
+def product64(x, w):
+    return x.double() @ w.double().T
+
+
+@pytest.mark.parametrize("L", [2, 3, 8])
+def test_many_short_batches_that_lie_apart(L):
+    """A part of longer rows: each batch has tiles of its own, and the result is that of the tokens together
+    within the sums' K u (|x| |W|) and half a step."""
+    x, w = rand(2000, 16, 128)[:, 2:2 + L], rand(264, 128, seed=1)
+    out = fn.linear_gate_residual(x, w)
+    want, size = product64(x, w), x.double().abs() @ w.double().abs().T
+    assert torch.all((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2 * 128 * 2.0 ** -24 * size)
+
+
+def test_x_that_repeats_rows():
+    x, w = rand(1, 2, 128), rand(264, 128, seed=1)
+    assert torch.equal(fn.linear_gate_residual(x.expand(2, 2, 128), w), fn.linear_gate_residual(x.repeat(2, 1, 1), w))
+    one = x[:, :1].expand(1, 4, 128)
+    assert torch.equal(fn.linear_gate_residual(one, w), fn.linear_gate_residual(one.contiguous(), w))
+    for apart in (x.expand(3, 2, 128), x[:, :1].expand(1, 5, 128)):
+        with pytest.raises(fn.FusedNormError, match="UNSUPPORTED"):
+            fn.linear_gate_residual(apart, w)
