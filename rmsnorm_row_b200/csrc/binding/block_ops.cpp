@@ -92,7 +92,8 @@ void check_shape(const Tensor& t, const char* name, c10::IntArrayRef shape, at::
   if (t.scalar_type() != dtype || t.sizes() != shape || t.device() != device)
     throw ValueError("%s must be a %s tensor of shape %s on %s", name, name_of(dtype), shape_of(shape).c_str(), device.str().c_str());
 }
-fn_operand rows_of(const Tensor& t) {  // of a (B, L, D) tensor
+// Of a (B, L, D) tensor. The stride along an extent of 1 means nothing (PyTorch leaves any there).
+fn_operand rows_of(const Tensor& t) {
   return fn_operand{t.data_ptr(), t.size(0) > 1 ? t.stride(0) : 0, 0, t.size(1) > 1 ? t.stride(1) : 0};
 }
 
@@ -289,7 +290,8 @@ ENTRY(norm_quant, 13) {
     r = a[11] == Py_None ? empty(x.sizes(), bf, device) : *tensor(a[11], "residual_out");
     check_shape(r, "residual_out", x.sizes(), bf, device);
     check_tensor(r, "residual_out", device, bf);
-    g.r = r.data_ptr(), g.r_stride_b = r.stride(0), g.r_stride_l = r.stride(1);
+    const fn_operand to = rows_of(r);
+    g.r = r.data_ptr(), g.r_stride_b = to.stride_b, g.r_stride_l = to.stride_l;
   }
   q = a[9] == Py_None ? empty(x.sizes(), at::kFloat8_e4m3fn, device) : *tensor(a[9], "out");
   check_shape(q, "out", x.sizes(), at::kFloat8_e4m3fn, device);
@@ -297,7 +299,8 @@ ENTRY(norm_quant, 13) {
   s = a[10] == Py_None ? empty({B, L}, at::kFloat, device) : *tensor(a[10], "row_scale_out");
   check_shape(s, "row_scale_out", {B, L}, at::kFloat, device);
   if (!s.is_contiguous()) throw ValueError("row_scale_out must be contiguous");
-  g.q = q.data_ptr(), g.q_stride_b = q.stride(0), g.q_stride_l = q.stride(1);
+  const fn_operand to = rows_of(q);
+  g.q = q.data_ptr(), g.q_stride_b = to.stride_b, g.q_stride_l = to.stride_l;
   g.row_scale = static_cast<float*>(s.data_ptr());
   const norm_quant_t h = handle_for(c, norm_quant_create, norm_quant_destroy, "norm_quant_create");
   check_status(norm_quant_launch(h, &g, place.stream()), "norm_quant_launch");
@@ -482,7 +485,8 @@ ENTRY(linear_gate, 10) {
   const Tensor out = a[8] == Py_None ? empty({B, L, N}, dtype, device) : *tensor(a[8], "out");
   check_shape(out, "out", {B, L, N}, dtype, device);
   check_tensor(out, "out", device, dtype);
-  g.out = out.data_ptr(), g.out_stride_b = out.stride(0), g.out_stride_l = out.stride(1);
+  const fn_operand to = rows_of(out);
+  g.out = out.data_ptr(), g.out_stride_b = to.stride_b, g.out_stride_l = to.stride_l;
   const linear_gate_t h = handle_for(c, linear_gate_create, linear_gate_destroy, "linear_gate_create");
   check_status(linear_gate_launch(h, &g, place.stream()), "linear_gate_launch");
   return wrap(a[8], out);

@@ -325,3 +325,20 @@ def test_x_that_repeats_rows():
     for apart in (x.expand(3, 2, 128), x[:, :1].expand(1, 5, 128)):
         with pytest.raises(fn.FusedNormError, match="UNSUPPORTED"):
             fn.linear_gate_residual(apart, w)
+
+
+@pytest.mark.parametrize("B,L", [(1, 7), (7, 1), (1, 1)])
+def test_strides_along_extents_of_one_mean_nothing(B, L):
+    def odd(t):
+        size, stride = t.shape, [s if n > 1 else 1 for n, s in zip(t.shape, t.stride())]
+        return t.as_strided(size, stride)
+
+    x, res, w = rand(B, L, 64), rand(B, L, 64, seed=1), rand(64, 64, seed=2)
+    q, r, out = (odd(torch.empty(B, L, 64, device="cuda", dtype=t)) for t in (torch.float8_e4m3fn, BF, BF))
+    want = fn.fused_residual_norm_scale_shift_quant(res, x, None, None, None, None, None)
+    got = fn.fused_residual_norm_scale_shift_quant(odd(res), odd(x), None, None, None, None, None, out=q, residual_out=r)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip((t.contiguous() for t in got), want))
+    assert torch.equal(fn.linear_gate_residual(odd(x), w, residual=odd(res), out=out), fn.linear_gate_residual(x, w, residual=res))
+    h, pos = x.view(B, L, 2, 32), torch.arange(L, device="cuda", dtype=torch.int32)[:, None]
+    y = odd(torch.empty_like(h))
+    assert torch.equal(fn.rope_norm(odd(h), pos, (16,), out=y), fn.rope_norm(h, pos, (16,)))
