@@ -80,19 +80,25 @@ fn_status validate(const linear_gate_s* h, const lg_args* a) {
 }
 
 // Where the matrix kernels say that a wait ran out: four bytes of host memory that every device
-// maps, for the life of the process. nullptr if there is none. The first call may be captured.
-int* gave_up_word() {
-  static int* const word = []() -> int* {
-    void* at = nullptr;
-    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-    cudaThreadExchangeStreamCaptureMode(&mode);
-    const cudaError_t e = cudaHostAlloc(&at, sizeof(int), cudaHostAllocPortable | cudaHostAllocMapped);
-    cudaThreadExchangeStreamCaptureMode(&mode);
-    if (e != cudaSuccess) return nullptr;
-    *static_cast<int*>(at) = 0;
-    return static_cast<int*>(at);
-  }();
-  return word;
+// maps, for the life of the process. The first call may be captured, or come from two threads.
+cudaError_t gave_up_word(int** word) {
+  static std::atomic<int*> known{nullptr};
+  if ((*word = known.load(std::memory_order_acquire))) return cudaSuccess;
+  void* at = nullptr;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return e;
+  e = cudaHostAlloc(&at, sizeof(int), cudaHostAllocPortable | cudaHostAllocMapped);
+  if (e == cudaSuccess) {
+    *(*word = static_cast<int*>(at)) = 0;
+    int* other = nullptr;
+    if (!known.compare_exchange_strong(other, *word, std::memory_order_acq_rel)) {
+      *word = other;
+      cudaFreeHost(at);
+    }
+  }
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  return e;
 }
 
 LinearOperand operand_of(const fn_operand& o) {
@@ -347,8 +353,8 @@ fn_status linear_gate_launch(linear_gate_t h, const lg_args* a, fn_stream_t stre
   const fn_status s = validate(h, a);
   if (s != FN_OK || a->B == 0 || a->L == 0) return s;
   LinearParams p = make_params(h, a);
-  p.gave_up = gave_up_word();
-  if (!p.gave_up) return launch_status(cudaErrorMemoryAllocation);
+  const cudaError_t e = gave_up_word(&p.gave_up);
+  if (e != cudaSuccess) return launch_status(e);
   const fn_status before = wait_status(p.gave_up);
   if (before != FN_OK) return before;
   if (p.rows <= (uint32_t)kTokens) return launch_tokens(h, p, reinterpret_cast<cudaStream_t>(stream));
