@@ -63,7 +63,7 @@ __device__ __forceinline__ float logistic_times(float z, float e) { return __fdi
 // GELU z Phi(z) of two values. Phi(-|z|) = erfc(|z| / sqrt 2) / 2 = e^(-z^2 / 2) s Q(s) with
 // s = 1 / (1 + 0.212 |z|): Q is the polynomial of degree 8 with the least largest relative error, 2e-8,
 // over |z| <= 13.5 (fitted by reweighted least squares). 1 + erf(z / sqrt 2) loses the value where
-// z < 0, and erfcf, as good, takes longer: 50000 x 2048 x 4096 553 us, with erff 570, with erfcf 698.
+// z < 0, and erfcf, as good, takes longer: 50000 x 2048 x 4096 555 us, with erff 568, with erfcf 698.
 // e^(-z^2 / 2) below 2^-126 (z < -13.2) is 0.
 __device__ __forceinline__ uint64_t gelu(uint64_t z) {
   using namespace fused_norm_impl;
@@ -88,18 +88,12 @@ __device__ __forceinline__ uint64_t gelu(uint64_t z) {
   return mul2(z, pk2(z0 > 0.0f ? 1.0f - a0 : a0, z1 > 0.0f ? 1.0f - a1 : a1));
 }
 
+// SiLU and GELU's tanh form.
 template <int N>
 __device__ __forceinline__ void activate(int act, float (&v)[N]) {
-  if (act == BO_ACT_NONE) return;
   if (act == BO_ACT_SILU) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = logistic_times(v[i], v[i]);
-  } else if (act == BO_ACT_GELU) {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      float unused;
-      fused_norm_impl::upk2(gelu(fused_norm_impl::pk2(v[i], v[N > 1 ? i + 1 : i])), v[i], N > 1 ? v[i + 1] : unused);
-    }
   } else {  // 1/2 (1 + tanh t) = 1 / (1 + e^-2t)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -169,7 +163,20 @@ struct Columns {
 #pragma unroll
       for (int i = 0; i < 16; ++i) z[i] = add2(z[i], pair(bias[i >> 2], i & 3));
     }
-    if (p.act != BO_ACT_NONE) {
+    if (p.act == BO_ACT_GELU) {
+      // In two halves: sixteen pairs' instructions at once cost the other activations up to 2% where a
+      // tile's epilogue runs once (999 x 2056 x 1288 with SiLU 19.0 against 18.7 us).
+#pragma unroll 1
+      for (int r = 0; r < 2; ++r) {
+        uint64_t t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = gelu(z[i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = z[i + 8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[8 + i] = t[i];
+      }
+    } else if (p.act != BO_ACT_NONE) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) upk2(z[i], v[2 * i], v[2 * i + 1]);
       activate(p.act, v);
@@ -680,7 +687,12 @@ __global__ void __launch_bounds__(kTokenThreads) linear_gate_tokens(const __grid
   auto one = [](const uint16_t* at) { return widen16<FP16>((uint32_t)*at).x; };
   if (p.bias) v += one(p.bias + n);
   float a[1] = {v};
-  activate(p.act, a);
+  if (p.act == BO_ACT_GELU) {
+    float same;
+    fused_norm_impl::upk2(gelu(fused_norm_impl::pk2(v, v)), a[0], same);
+  } else if (p.act != BO_ACT_NONE) {
+    activate(p.act, a);
+  }
   v = a[0];
   const uint16_t* e = p.residual.ptr + (r.b * p.residual.sb + r.l * p.residual.sl) + n;
   if (r.gate && p.has_residual) v = fmaf(one(r.gate + n), v, one(e));
