@@ -17,7 +17,7 @@
 // against 7.2 ms.
 //
 // A few tokens: every warp streams rows of W past the tokens with 16-byte loads; one token against
-// 30720 rows of 5120 takes 48 us, the copy rate.
+// 30720 rows of 5120 takes 48 to 50 us, 97% of the copy rate.
 #pragma once
 
 #include <cuda_fp8.h>

@@ -19,7 +19,7 @@
 // neighbouring vectors. A norm over the head is a shuffle inside W lanes.
 //
 // B200, 40 heads of 128: 176400 tokens forward 639 us, 5.7 TB/s of the 6.6 of a plain copy (1730
-// instructions a row); gradient of 90000 tokens 588 us, 4.7 TB/s (4100 a row, issue 58% busy).
+// instructions a row); gradient of 90000 tokens 553 to 597 us, 4.7 TB/s (4100 a row, issue 58% busy).
 #pragma once
 
 #include "../../../include/block_ops.h"
