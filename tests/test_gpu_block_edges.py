@@ -342,3 +342,21 @@ def test_strides_along_extents_of_one_mean_nothing(B, L):
     h, pos = x.view(B, L, 2, 32), torch.arange(L, device="cuda", dtype=torch.int32)[:, None]
     y = odd(torch.empty_like(h))
     assert torch.equal(fn.rope_norm(odd(h), pos, (16,), out=y), fn.rope_norm(h, pos, (16,)))
+
+
+@pytest.mark.parametrize("rows", [3, 3000])
+@pytest.mark.parametrize("D", [16, 48, 80, 2320, 5120, 5136, 10256, 16384])
+def test_rows_of_one_value_are_zero_under_layernorm(D, rows):
+    """r - mean is 0 throughout, so y is the bias, or a row of zeros with row_scale 1."""
+    values = torch.tensor([1.0, -3.0, 300.0, 1e38, -1e-30, 0.1, 7e20, 0.0], device="cuda").to(BF)
+    x = values[torch.arange(rows, device="cuda") % 8][None, :, None].expand(1, rows, D).contiguous()
+    q, s = fn.norm_scale_shift_quant(x, None, None, None, None, "layer", 1e-6)
+    assert (s == 1).all() and (q.float() == 0).all()
+    bias = rand(D, seed=1)
+    q, s = fn.norm_scale_shift_quant(x, None, bias, None, None, "layer", 1e-6)
+    top = bias.float().abs().max()
+    assert torch.equal(s, (top.double() / 448).float().expand_as(s))  # (a float by a scalar is a product in torch)
+    near = (bias.double() * 448 / top.double()).float()
+    lo, hi = ((near * (1 + e * 2.0 ** -22)).to(torch.float8_e4m3fn).float() for e in (-1, 1))
+    got = q.float()
+    assert torch.all((got >= torch.minimum(lo, hi)) & (got <= torch.maximum(lo, hi)))
