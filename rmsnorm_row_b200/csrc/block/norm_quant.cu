@@ -225,7 +225,11 @@ __device__ __forceinline__ Stats statistics(const QuantParams& p, const Group& g
 #pragma unroll
         for (int i = 0; i < 4; ++i) c += bf16_f64<0>(word(u, i)) + bf16_f64<1>(word(u, i));
       }
-      mu = g.sum(c, g.sh->again[0]) * p.inv_d;
+      // 1 / D is rounded: one correction gives the rounded quotient, so that the mean of equal values is
+      // that value and their row is zero.
+      c = g.sum(c, g.sh->again[0]);
+      mu = c * p.inv_d;
+      mu = fma(fma(-mu, 8.0 * p.vecs, c), p.inv_d, mu);
       c = 0.0;
     }
 #pragma unroll 1
