@@ -114,6 +114,8 @@ fn_status norm_quant_destroy(norm_quant_t h);
  * BO_NORM_HEAD) of dn x rho, in a fixed order: in fp32 over runs of at most 512 tokens of a thread
  * (up to 4 heads of each for BO_NORM_HEAD, so an error of at most 2048 2^-24 of the terms'
  * magnitudes), in fp64 across threads; a CTA's runs are added in fp32.
+ * Terms w dn x below fp32's normal numbers are lost: x and grad of a row are to have a product above
+ * 2^-100.
  */
 typedef struct rope_norm_s* rope_norm_t;
 
