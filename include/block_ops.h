@@ -15,8 +15,8 @@
  * asynchronous on the caller's stream and go to the calling thread's current device (the
  * one that owns the stream and the buffers), argument errors found on the host before
  * anything is launched, outputs untouched on an error, no allocation (but four bytes of host
- * memory that linear_gate's first launch takes for good), no synchronisation, no fallback. All buffers are the caller's. Sizes with a zero are valid and launch
- * nothing. A non-zero stride need not be larger than the extent it steps over on inputs
+ * memory that linear_gate's first launch takes for good), no synchronisation, no fallback. All
+ * buffers are the caller's. Sizes with a zero are valid and launch nothing. A non-zero stride need not be larger than the extent it steps over on inputs
  * (rows may overlap); output rows must not overlap each other or an input, except where a
  * call says so.
  */
